@@ -17,6 +17,17 @@ Functions carry the C names (see include/fp8bs.h for the full contract):
     fp8_grouped_gemm(offsets, a, sa, b, sb, out_dtype, rows_bound=None)    -> d
     fp8_grouped_gemm_strided(offsets, a, sa, G, N, b, ldb, b_estride, sb, ...) -> d
 
+and the feed-forward block around them (block.py):
+
+    fp8_gated_gemm(a, sa, b, sb, act, out_dtype)              -> (d, gu)
+    fp8_gated_gemm_quant(a, sa, b, sb, act, scale_mode)       -> (q, s, gu)
+    fp8_grouped_gated_gemm[_quant](offsets, a, sa, b, sb, act, ...)
+    fp8_gated_backward(dh, gu, act, scale_mode)               -> (qr, sr, qc, sc, qh, sh)
+    fp8_grouped_gated_backward(offsets, dh, gu, ...)          -> the same
+    fp8_norm_residual(x, w_pre, y, w_post, gate, ...)         -> (xo, h, q, s, rstd_y, rstd_x)
+    fp8_norm_residual_backward(dxo, dh, xo, rstd_x, w_pre, ...) -> (dx, dy, dw_pre, dw_post, dgate)
+    fp8_grad_norm(grads) -> norm;  fp8_grad_clip(grads, max_norm, out=None) -> (norm, coef)
+
 bf16 inputs are ``torch.bfloat16`` tensors (their bit patterns are what the
 library reads); codes are ``torch.uint8``; scales ``torch.float32``.
 """
@@ -94,6 +105,7 @@ def lib():
         L.fp8_gemm_blockscaled_quant.restype = i32
         L.fp8_gemm_blockscaled_quant.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i32, i64, i64, i32,
                                                  vp, i64, vp, i64, i32, vp]
+        block.declare(L)
         _lib = L
     return _lib
 
@@ -449,3 +461,10 @@ def linear_dgrad(qdy, sdy, qwt, sw, out_dtype=OUT_F32, accum=ACCUM_FP32):
 def linear_wgrad(qdyt, sdyt, qxt, sxt, out_dtype=OUT_F32, accum=ACCUM_FP32):
     """dW = dY^T X from quant_tile(dY, COL) and quant_tile(X, COL)."""
     return fp8_gemm_blockscaled(qdyt, sdyt, qxt, sxt, BSCALE_TILE, _ld(sxt), 0, out_dtype, accum=accum)
+
+
+from . import block  # noqa: E402  (needs the names above)
+from .block import (ACT_GELU, ACT_SILU, NormResidual, NormResidualGrads, fp8_gated_backward,  # noqa: E402,F401
+                    fp8_gated_gemm, fp8_gated_gemm_quant, fp8_grad_clip, fp8_grad_norm, fp8_grouped_gated_backward,
+                    fp8_grouped_gated_gemm, fp8_grouped_gated_gemm_quant, fp8_norm_residual,
+                    fp8_norm_residual_backward, gated_workspace_bytes)

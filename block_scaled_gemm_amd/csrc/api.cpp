@@ -5,42 +5,13 @@
 // gfx950, then enqueues its kernels on the caller's stream.
 #include <hip/hip_runtime.h>
 
-#include <cstring>
 #include <mutex>
 
 #include "../../include/fp8bs.h"
+#include "api_util.h"
 #include "kernels.h"
 
-#define FP8BS_EXPORT extern "C" __attribute__((visibility("default")))
-
-namespace {
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-// gfx950 check, cached per device ordinal.
-int check_device() {
-    static std::mutex mu;
-    static int cache[64];  // 0 unknown, 1 ok, 2 not ok
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return FP8BS_ERR_DEVICE;
-    if (dev < 64) {
-        std::lock_guard<std::mutex> lk(mu);
-        if (cache[dev] == 1) return FP8BS_OK;
-        if (cache[dev] == 2) return FP8BS_ERR_DEVICE;
-    }
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return FP8BS_ERR_DEVICE;
-    const bool ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    if (dev < 64) {
-        std::lock_guard<std::mutex> lk(mu);
-        cache[dev] = ok ? 1 : 2;
-    }
-    return ok ? FP8BS_OK : FP8BS_ERR_DEVICE;
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? FP8BS_OK : FP8BS_ERR_HIP; }
-
-}  // namespace
+using namespace fp8bs_api;
 
 FP8BS_EXPORT int fp8bs_abi_version(void) { return FP8BS_ABI_VERSION; }
 

@@ -1,0 +1,497 @@
+// block_api.cpp -- the C ABI's feed-forward block entry points (declared in
+// include/fp8bs.h): the gated products and their backward pass, the norms
+// around a block, and gradient clipping.  As in api.cpp, every argument is
+// checked on the host before any HIP call is made.
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "api_util.h"
+#include "block_kernels.h"
+#include "kernels.h"
+
+using namespace fp8bs_api;
+
+namespace {
+
+// Bytes between the gate's and the up's block scalars, and element offsets
+// inside a tile, are 32-bit in the kernels.
+constexpr int64_t kMaxScaleSpan = 1LL << 30;
+constexpr int64_t kMaxGrid = (1LL << 31) - 1;  // workgroups of one launch
+
+bool bad_act(int act) { return act != FP8BS_ACT_SILU && act != FP8BS_ACT_GELU; }
+bool bad_mode(int m) { return m != FP8BS_SCALE_FP32 && m != FP8BS_SCALE_POW2; }
+bool bad_accum(int a) { return a != FP8BS_ACCUM_FP32 && a != FP8BS_ACCUM_MFMA8 && a != FP8BS_ACCUM_MFMA8_POW2; }
+
+// Operands, shape and the kept pre-activations of a gated product.
+int check_gated(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa,
+                const uint8_t* b, int64_t ldb, const float* sb, int64_t ldsb, int act, const uint16_t* gu,
+                int64_t ldgu, int accum) {
+    if (bad_act(act) || bad_accum(accum) || M < 0 || N < 0 || K < 0) return FP8BS_ERR_ARG;
+    if (M > 0 && N > 0 && K > 0 && (!a || !sa || !b || !sb)) return FP8BS_ERR_ARG;
+    if (K % 128 != 0 || N % 128 != 0) return FP8BS_ERR_SHAPE;
+    if (lda > FP8BS_MAX_LD || ldb > FP8BS_MAX_LD) return FP8BS_ERR_SHAPE;
+    if (lda < K || ldb < K || ldsa < M || ldsb < K / 128 || (gu && ldgu < 2 * N)) return FP8BS_ERR_ARG;
+    if (N / 128 > 0 && ldsb > kMaxScaleSpan / (N / 128)) return FP8BS_ERR_SHAPE;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sa, 4) || !aligned(sb, 4) || !aligned(gu, 16) ||
+        (K > 0 && (lda % 16 != 0 || ldb % 16 != 0)) || (gu && ldgu % 8 != 0))
+        return FP8BS_ERR_ALIGN;
+    return FP8BS_OK;
+}
+
+int check_out(int64_t M, int64_t N, const void* d, int64_t ldd, int out_dtype) {
+    if (out_dtype != FP8BS_OUT_BF16 && out_dtype != FP8BS_OUT_F32) return FP8BS_ERR_ARG;
+    if ((M > 0 && N > 0 && !d) || ldd < N) return FP8BS_ERR_ARG;
+    return !aligned(d, 16) || ldd % 4 != 0 ? FP8BS_ERR_ALIGN : FP8BS_OK;
+}
+
+int check_out_quant(int64_t M, int64_t N, int scale_mode, const uint8_t* q, int64_t ldq, const float* s,
+                    int64_t lds) {
+    if (bad_mode(scale_mode)) return FP8BS_ERR_ARG;
+    if ((M > 0 && N > 0 && (!q || !s)) || ldq < N || lds < M) return FP8BS_ERR_ARG;
+    return !aligned(q, 4) || !aligned(s, 4) || ldq % 4 != 0 ? FP8BS_ERR_ALIGN : FP8BS_OK;
+}
+
+fp8bs::GatedArgs gated_args(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const float* sa,
+                            int64_t ldsa, const uint8_t* b, int64_t ldb, const float* sb, int64_t ldsb, int act,
+                            uint16_t* gu, int64_t ldgu, int accum) {
+    fp8bs::GatedArgs g{};
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.a = a;
+    g.lda = lda;
+    g.sa = sa;
+    g.ldsa = ldsa;
+    g.b = b;
+    g.ldb = ldb;
+    g.sb = sb;
+    g.ldsb = ldsb;
+    g.act = act;
+    g.gu = gu;
+    g.ldgu = ldgu;
+    g.accum = accum;
+    g.splits = 1;
+    return g;
+}
+
+void set_out(fp8bs::GatedArgs& g, void* d, int64_t ldd, int out_dtype) {
+    g.out = out_dtype == FP8BS_OUT_F32 ? fp8bs::GATED_F32 : fp8bs::GATED_BF16;
+    g.d = d;
+    g.ldd = ldd;
+}
+
+void set_out_quant(fp8bs::GatedArgs& g, int scale_mode, uint8_t* q, int64_t ldq, float* s, int64_t lds) {
+    g.out = scale_mode == FP8BS_SCALE_POW2 ? fp8bs::GATED_QUANT_POW2 : fp8bs::GATED_QUANT;
+    g.d = q;
+    g.ldd = ldq;
+    g.qs = s;
+    g.qlds = lds;
+}
+
+int run_dense(fp8bs::GatedArgs& g, void* workspace, size_t workspace_bytes, void* stream) {
+    if (g.M == 0 || g.N == 0) return FP8BS_OK;
+    if ((g.M + 63) / 64 > kMaxGrid / (g.N / 128)) return FP8BS_ERR_SHAPE;
+    const size_t need = fp8bs::gated_workspace(g.M, g.N, g.K);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return FP8BS_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 16)) return FP8BS_ERR_ALIGN;
+    if (int r = check_device()) return r;
+    g.splits = need > 0 ? fp8bs::gated_splits(g.M, g.N, g.K) : 1;
+    g.ws = (float*)workspace;
+    return hip_status(fp8bs::launch_gated(g, (hipStream_t)stream));
+}
+
+int run_grouped(fp8bs::GatedArgs& g, int G, const int32_t* offsets, void* stream) {
+    if (G == 0 || g.M == 0 || g.N == 0) return FP8BS_OK;
+    if (G > kMaxGrid / (g.N / 128)) return FP8BS_ERR_SHAPE;
+    if (int r = check_device()) return r;
+    g.G = G;
+    g.offsets = offsets;
+    g.b_estride = 2 * g.N * g.K;
+    g.sb_estride = (2 * g.N / 128) * (g.K / 128);
+    return hip_status(fp8bs::launch_grouped_gated(g, (hipStream_t)stream));
+}
+
+int check_offsets(int G, const int32_t* offsets) {
+    if (G < 0 || (G > 0 && !offsets)) return FP8BS_ERR_ARG;
+    return aligned(offsets, 4) ? FP8BS_OK : FP8BS_ERR_ALIGN;
+}
+
+}  // namespace
+
+FP8BS_EXPORT size_t fp8_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0 || K <= 0 || N % 128 != 0 || K % 128 != 0) return 0;
+    return fp8bs::gated_workspace(M, N, K);
+}
+
+FP8BS_EXPORT int fp8_gated_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const float* sa,
+                                int64_t ldsa, const uint8_t* b, int64_t ldb, const float* sb, int64_t ldsb, int act,
+                                void* d, int64_t ldd, int out_dtype, uint16_t* gu, int64_t ldgu, int accum,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    if (int r = check_gated(M, N, K, a, lda, sa, ldsa, b, ldb, sb, ldsb, act, gu, ldgu, accum)) return r;
+    if (int r = check_out(M, N, d, ldd, out_dtype)) return r;
+    fp8bs::GatedArgs g = gated_args(M, N, K, a, lda, sa, ldsa, b, ldb, sb, ldsb, act, gu, ldgu, accum);
+    set_out(g, d, ldd, out_dtype);
+    return run_dense(g, workspace, workspace_bytes, stream);
+}
+
+FP8BS_EXPORT int fp8_gated_gemm_quant(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda,
+                                      const float* sa, int64_t ldsa, const uint8_t* b, int64_t ldb, const float* sb,
+                                      int64_t ldsb, int act, int scale_mode, uint8_t* q, int64_t ldq, float* s,
+                                      int64_t lds, uint16_t* gu, int64_t ldgu, int accum, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+    if (int r = check_gated(M, N, K, a, lda, sa, ldsa, b, ldb, sb, ldsb, act, gu, ldgu, accum)) return r;
+    if (int r = check_out_quant(M, N, scale_mode, q, ldq, s, lds)) return r;
+    fp8bs::GatedArgs g = gated_args(M, N, K, a, lda, sa, ldsa, b, ldb, sb, ldsb, act, gu, ldgu, accum);
+    set_out_quant(g, scale_mode, q, ldq, s, lds);
+    return run_dense(g, workspace, workspace_bytes, stream);
+}
+
+FP8BS_EXPORT int fp8_grouped_gated_gemm(int G, int64_t rows_bound, int64_t N, int64_t K, const int32_t* offsets,
+                                        const uint8_t* a, int64_t lda, const float* sa, int64_t ldsa,
+                                        const uint8_t* b, const float* sb, int act, void* d, int64_t ldd,
+                                        int out_dtype, uint16_t* gu, int64_t ldgu, int accum, void* stream) {
+    if (int r = check_offsets(G, offsets)) return r;
+    if (int r = check_gated(rows_bound, N, K, a, lda, sa, ldsa, b, K, sb, K / 128, act, gu, ldgu, accum)) return r;
+    if (int r = check_out(rows_bound, N, d, ldd, out_dtype)) return r;
+    fp8bs::GatedArgs g = gated_args(rows_bound, N, K, a, lda, sa, ldsa, b, K, sb, K / 128, act, gu, ldgu, accum);
+    set_out(g, d, ldd, out_dtype);
+    return run_grouped(g, G, offsets, stream);
+}
+
+FP8BS_EXPORT int fp8_grouped_gated_gemm_quant(int G, int64_t rows_bound, int64_t N, int64_t K,
+                                              const int32_t* offsets, const uint8_t* a, int64_t lda, const float* sa,
+                                              int64_t ldsa, const uint8_t* b, const float* sb, int act,
+                                              int scale_mode, uint8_t* q, int64_t ldq, float* s, int64_t lds,
+                                              uint16_t* gu, int64_t ldgu, int accum, void* stream) {
+    if (int r = check_offsets(G, offsets)) return r;
+    if (int r = check_gated(rows_bound, N, K, a, lda, sa, ldsa, b, K, sb, K / 128, act, gu, ldgu, accum)) return r;
+    if (int r = check_out_quant(rows_bound, N, scale_mode, q, ldq, s, lds)) return r;
+    fp8bs::GatedArgs g = gated_args(rows_bound, N, K, a, lda, sa, ldsa, b, K, sb, K / 128, act, gu, ldgu, accum);
+    set_out_quant(g, scale_mode, q, ldq, s, lds);
+    return run_grouped(g, G, offsets, stream);
+}
+
+// ---- backward ---------------------------------------------------------------------------
+
+namespace {
+
+int gated_backward(int64_t M, int64_t N, int G, const int32_t* offsets, int64_t bound, const uint16_t* dh,
+                   int64_t lddh, const uint16_t* gu, int64_t ldgu, int act, int scale_mode, uint8_t* qr, int64_t ldqr,
+                   float* sr, int64_t ldsr, uint8_t* qc, int64_t ldqc, float* sc, int64_t ldsc, uint8_t* qh,
+                   int64_t ldqh, float* sh, int64_t ldsh, void* stream) {
+    if (bad_act(act) || bad_mode(scale_mode) || M < 0 || N < 0) return FP8BS_ERR_ARG;
+    if (M > 0 && N > 0 && (!dh || !gu || (!qr && !qc && !qh))) return FP8BS_ERR_ARG;
+    if ((qr && !sr) || (qc && !sc) || (qh && !sh)) return FP8BS_ERR_ARG;
+    if (N % 128 != 0) return FP8BS_ERR_SHAPE;
+    if (lddh < N || ldgu < 2 * N || (qr && (ldqr < 2 * N || ldsr < M)) ||
+        (qc && (ldqc < bound || ldsc < 2 * N)) || (qh && (ldqh < bound || ldsh < N)))
+        return FP8BS_ERR_ARG;
+    if (!aligned(dh, 16) || !aligned(gu, 16) || !aligned(qr, 16) || !aligned(qc, 16) || !aligned(qh, 16) ||
+        !aligned(sr, 4) || !aligned(sc, 4) || !aligned(sh, 4) || lddh % 8 != 0 || ldgu % 8 != 0 ||
+        (qr && ldqr % 16 != 0) || (qc && ldqc % 16 != 0) || (qh && ldqh % 16 != 0))
+        return FP8BS_ERR_ALIGN;
+    if (M == 0 || N == 0) return FP8BS_OK;
+    if (bound / 128 > kMaxGrid / (N / 128)) return FP8BS_ERR_SHAPE;
+    if (int r = check_device()) return r;
+    fp8bs::GatedBwdArgs g{};
+    g.M = M;
+    g.N = N;
+    g.dh = dh;
+    g.lddh = lddh;
+    g.gu = gu;
+    g.ldgu = ldgu;
+    g.act = act;
+    g.pow2 = scale_mode == FP8BS_SCALE_POW2;
+    g.qr = qr;
+    g.ldqr = ldqr;
+    g.sr = sr;
+    g.ldsr = ldsr;
+    g.qc = qc;
+    g.ldqc = ldqc;
+    g.sc = sc;
+    g.ldsc = ldsc;
+    g.qh = qh;
+    g.ldqh = ldqh;
+    g.sh = sh;
+    g.ldsh = ldsh;
+    g.offsets = offsets;
+    g.G = G;
+    return hip_status(fp8bs::launch_gated_backward(g, (hipStream_t)stream));
+}
+
+}  // namespace
+
+FP8BS_EXPORT int fp8_gated_backward(int64_t M, int64_t N, const uint16_t* dh, int64_t lddh, const uint16_t* gu,
+                                    int64_t ldgu, int act, int scale_mode, uint8_t* qr, int64_t ldqr, float* sr,
+                                    int64_t ldsr, uint8_t* qc, int64_t ldqc, float* sc, int64_t ldsc, uint8_t* qh,
+                                    int64_t ldqh, float* sh, int64_t ldsh, void* stream) {
+    const int64_t bound = M > 0 ? (M + 127) / 128 * 128 : 0;
+    return gated_backward(M, N, 0, nullptr, bound, dh, lddh, gu, ldgu, act, scale_mode, qr, ldqr, sr, ldsr, qc, ldqc,
+                          sc, ldsc, qh, ldqh, sh, ldsh, stream);
+}
+
+FP8BS_EXPORT int fp8_grouped_gated_backward(int G, const int32_t* offsets, int64_t T, int64_t N, const uint16_t* dh,
+                                            int64_t lddh, const uint16_t* gu, int64_t ldgu, int act, int scale_mode,
+                                            uint8_t* qr, int64_t ldqr, float* sr, int64_t ldsr, uint8_t* qc,
+                                            int64_t ldqc, float* sc, int64_t ldsc, uint8_t* qh, int64_t ldqh,
+                                            float* sh, int64_t ldsh, void* stream) {
+    if (int r = check_offsets(G, offsets)) return r;
+    if (T < 0) return FP8BS_ERR_ARG;
+    if (G == 0) T = 0;
+    return gated_backward(T, N, G, offsets, fp8bs::grouped_col_bound(T, G), dh, lddh, gu, ldgu, act, scale_mode, qr,
+                          ldqr, sr, ldsr, qc, ldqc, sc, ldsc, qh, ldqh, sh, ldsh, stream);
+}
+
+// ---- norms --------------------------------------------------------------------------------
+
+FP8BS_EXPORT int fp8_norm_residual(int64_t M, int64_t D, const uint16_t* x, int64_t ldx, const uint16_t* y,
+                                   int64_t ldy, const float* w_post, const float* gate, int64_t gate_rows,
+                                   float alpha, float eps, uint16_t* xo, int64_t ldxo, const float* w_pre,
+                                   uint16_t* h, int64_t ldh, int scale_mode, uint8_t* q, int64_t ldq, float* s,
+                                   int64_t lds, float* rstd_y, float* rstd_x, void* stream) {
+    if (M < 0 || D < 0 || bad_mode(scale_mode)) return FP8BS_ERR_ARG;
+    if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(alpha)) return FP8BS_ERR_ARG;
+    if (gate && gate_rows < 1) return FP8BS_ERR_ARG;
+    if (M > 0 && D > 0) {  // (a matrix of no rows may be a null pointer)
+        // without y there is no residual sum; without w_pre no next norm; one of the two has to be asked for
+        if (!y && (w_post || gate || xo || rstd_y)) return FP8BS_ERR_ARG;
+        if (!w_pre && (h || q || s || rstd_x)) return FP8BS_ERR_ARG;
+        if ((rstd_y && !w_post) || (q != nullptr) != (s != nullptr)) return FP8BS_ERR_ARG;
+        if (!x || (y && !xo) || (!y && !w_pre) || (w_pre && !h && !q)) return FP8BS_ERR_ARG;
+    }
+    if (D % 8 != 0 || (q && D % 128 != 0) || D > fp8bs::NORM_MAX_COLS) return FP8BS_ERR_SHAPE;
+    if (ldx < D || (y && (ldy < D || ldxo < D)) || (h && ldh < D) || (q && (ldq < D || lds < M))) return FP8BS_ERR_ARG;
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(xo, 16) || !aligned(h, 16) || !aligned(q, 16) ||
+        !aligned(w_post, 16) || !aligned(w_pre, 16) || !aligned(gate, 16) || !aligned(s, 4) || !aligned(rstd_y, 4) ||
+        !aligned(rstd_x, 4) || ldx % 8 != 0 || (y && (ldy % 8 != 0 || ldxo % 8 != 0)) || (h && ldh % 8 != 0) ||
+        (q && ldq % 16 != 0))
+        return FP8BS_ERR_ALIGN;
+    if (M == 0 || D == 0) return FP8BS_OK;
+    if (M > kMaxGrid) return FP8BS_ERR_SHAPE;
+    if (int r = check_device()) return r;
+    fp8bs::NormArgs g{};
+    g.M = M;
+    g.D = D;
+    g.x = x;
+    g.ldx = ldx;
+    g.y = y;
+    g.ldy = ldy;
+    g.w_post = w_post;
+    g.gate = gate;
+    g.gate_rows = gate_rows;
+    g.alpha = alpha;
+    g.eps = eps;
+    g.xo = xo;
+    g.ldxo = ldxo;
+    g.w_pre = w_pre;
+    g.h = h;
+    g.ldh = ldh;
+    g.q = q;
+    g.ldq = ldq;
+    g.s = s;
+    g.lds = lds;
+    g.pow2 = scale_mode == FP8BS_SCALE_POW2;
+    g.rstd_y = rstd_y;
+    g.rstd_x = rstd_x;
+    return hip_status(fp8bs::launch_norm(g, (hipStream_t)stream));
+}
+
+FP8BS_EXPORT size_t fp8_norm_backward_workspace_bytes(int64_t M, int64_t D) {
+    if (M <= 0 || D <= 0) return 0;
+    return fp8bs::norm_bwd_workspace(M, D);
+}
+
+FP8BS_EXPORT int fp8_norm_residual_backward(int64_t M, int64_t D, const uint16_t* dxo, int64_t lddxo,
+                                            const uint16_t* dh, int64_t lddh, const uint16_t* xo, int64_t ldxo,
+                                            const float* rstd_x, const float* w_pre, const uint16_t* y, int64_t ldy,
+                                            const float* rstd_y, const float* w_post, const float* gate,
+                                            int64_t gate_rows, float alpha, uint16_t* dx, int64_t lddx, uint16_t* dy,
+                                            int64_t lddy, float* dw_pre, float* dw_post, float* dgate,
+                                            void* workspace, size_t workspace_bytes, void* stream) {
+    if (M < 0 || D < 0 || !std::isfinite(alpha)) return FP8BS_ERR_ARG;
+    if (gate && gate_rows < 1) return FP8BS_ERR_ARG;
+    if (M > 0 && D > 0) {  // (a matrix of no rows may be a null pointer)
+        if (!y && (w_post || gate || dy)) return FP8BS_ERR_ARG;
+        if ((!dxo && !dh) || !dx || (y && !dy)) return FP8BS_ERR_ARG;
+        if (dh ? !w_pre || !xo || !rstd_x || !dw_pre : dw_pre != nullptr) return FP8BS_ERR_ARG;
+        if (w_post ? !rstd_y || !dw_post : dw_post != nullptr) return FP8BS_ERR_ARG;
+        if ((gate != nullptr) != (dgate != nullptr)) return FP8BS_ERR_ARG;
+    }
+    if (D % 8 != 0 || D > fp8bs::NORM_MAX_COLS) return FP8BS_ERR_SHAPE;
+    if ((dxo && lddxo < D) || (dh && (lddh < D || ldxo < D)) || (y && (ldy < D || lddy < D)) || lddx < D)
+        return FP8BS_ERR_ARG;
+    if (!aligned(dxo, 16) || !aligned(dh, 16) || !aligned(xo, 16) || !aligned(y, 16) || !aligned(dx, 16) ||
+        !aligned(dy, 16) || !aligned(w_pre, 16) || !aligned(w_post, 16) || !aligned(gate, 16) ||
+        !aligned(dgate, 16) || !aligned(dw_pre, 4) || !aligned(dw_post, 4) || !aligned(rstd_x, 4) ||
+        !aligned(rstd_y, 4) || (dxo && lddxo % 8 != 0) || (dh && (lddh % 8 != 0 || ldxo % 8 != 0)) ||
+        (y && (ldy % 8 != 0 || lddy % 8 != 0)) || lddx % 8 != 0)
+        return FP8BS_ERR_ALIGN;
+    if (D == 0) return FP8BS_OK;
+    const size_t need = fp8_norm_backward_workspace_bytes(M, D);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return FP8BS_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 16)) return FP8BS_ERR_ALIGN;
+    if (int r = check_device()) return r;
+    fp8bs::NormBwdArgs g{};
+    g.M = M;
+    g.D = D;
+    g.dxo = dxo;
+    g.lddxo = lddxo;
+    g.dh = dh;
+    g.lddh = lddh;
+    g.xo = xo;
+    g.ldxo = ldxo;
+    g.rstd_x = rstd_x;
+    g.w_pre = w_pre;
+    g.y = y;
+    g.ldy = ldy;
+    g.rstd_y = rstd_y;
+    g.w_post = w_post;
+    g.gate = gate;
+    g.gate_rows = gate_rows;
+    g.alpha = alpha;
+    g.dx = dx;
+    g.lddx = lddx;
+    g.dy = dy;
+    g.lddy = lddy;
+    g.dw_pre = dw_pre;
+    g.dw_post = dw_post;
+    g.dgate = dgate;
+    g.ws = (float*)workspace;
+    g.parts = fp8bs::norm_bwd_parts(M);
+    return hip_status(fp8bs::launch_norm_bwd(g, (hipStream_t)stream));
+}
+
+// ---- gradient norm and clipping -------------------------------------------------------------
+
+namespace {
+
+int64_t clip_chunks(int64_t count) { return (count + fp8bs::CLIP_CHUNK - 1) / fp8bs::CLIP_CHUNK; }
+
+size_t clip_parts_bound(int64_t n) {
+    const int64_t tables = (n + fp8bs::CLIP_TABLE - 1) / fp8bs::CLIP_TABLE;
+    return (size_t)(tables > 0 ? tables : 1) * (size_t)fp8bs::clip_grid((int64_t)1 << 40, tables);
+}
+
+int check_grads(int64_t n, const void* const* g, const int64_t* count, const int32_t* dtype) {
+    if (n < 0 || (n > 0 && (!g || !count || !dtype))) return FP8BS_ERR_ARG;
+    for (int64_t i = 0; i < n; i++) {
+        if (dtype[i] != FP8BS_OUT_BF16 && dtype[i] != FP8BS_OUT_F32) return FP8BS_ERR_ARG;
+        if (count[i] < 0 || (count[i] > 0 && !g[i])) return FP8BS_ERR_ARG;
+        if (count[i] > FP8BS_MAX_GRAD) return FP8BS_ERR_SHAPE;  // a table's chunks are counted in 32 bits
+    }
+    for (int64_t i = 0; i < n; i++)
+        if (!aligned(g[i], dtype[i] == FP8BS_OUT_F32 ? 4 : 2)) return FP8BS_ERR_ALIGN;
+    return FP8BS_OK;
+}
+
+// Each output is its own gradient or apart from every gradient and every
+// other output.  May throw std::bad_alloc.
+bool outputs_apart(int64_t n, const void* const* g, void* const* out, const int64_t* count, const int32_t* dtype) {
+    struct Range {
+        uintptr_t lo, hi;
+        bool write;
+    };
+    std::vector<Range> r;
+    r.reserve((size_t)(2 * n));
+    for (int64_t i = 0; i < n; i++) {
+        if (count[i] == 0) continue;
+        const uintptr_t bytes = (uintptr_t)count[i] * (dtype[i] == FP8BS_OUT_F32 ? 4 : 2);
+        r.push_back({(uintptr_t)out[i], (uintptr_t)out[i] + bytes, true});
+        if (out[i] != g[i]) r.push_back({(uintptr_t)g[i], (uintptr_t)g[i] + bytes, false});
+    }
+    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    uintptr_t any_end = 0, write_end = 0;  // furthest ends of the ranges before
+    for (const Range& x : r) {
+        if (x.lo < write_end || (x.write && x.lo < any_end)) return false;
+        any_end = std::max(any_end, x.hi);
+        if (x.write) write_end = std::max(write_end, x.hi);
+    }
+    return true;
+}
+
+// Runs f(table, grid) for each launch's worth of tensors.
+template <typename F>
+hipError_t each_table(int64_t n, const void* const* g, void* const* out, const int64_t* count, const int32_t* dtype,
+                      F f) {
+    const int64_t tables = (n + fp8bs::CLIP_TABLE - 1) / fp8bs::CLIP_TABLE;
+    for (int64_t k = 0; k < tables; k++) {
+        fp8bs::ClipTable t{};
+        int64_t chunks = 0;
+        const int64_t end = std::min(n, (k + 1) * fp8bs::CLIP_TABLE);
+        for (int64_t i = k * fp8bs::CLIP_TABLE; i < end; i++) {
+            if (count[i] == 0) continue;  // every tensor of a table owns a chunk
+            t.g[t.n] = g[i];
+            t.out[t.n] = out ? out[i] : nullptr;
+            t.count[t.n] = count[i];
+            t.f32[t.n] = dtype[i] == FP8BS_OUT_F32;
+            t.first[t.n] = (int32_t)chunks;
+            chunks += clip_chunks(count[i]);
+            t.n++;
+        }
+        t.first[t.n] = (int32_t)chunks;
+        if (t.n == 0) continue;
+        const hipError_t e = f(t, fp8bs::clip_grid(chunks, tables));
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+FP8BS_EXPORT size_t fp8_grad_workspace_bytes(int64_t n) { return n < 0 ? 0 : clip_parts_bound(n) * sizeof(double); }
+
+FP8BS_EXPORT int fp8_grad_norm(int64_t n, const void* const* g, const int64_t* count, const int32_t* dtype,
+                               float* norm, void* workspace, size_t workspace_bytes, void* stream) {
+    if (int r = check_grads(n, g, count, dtype)) return r;
+    if (!norm) return FP8BS_ERR_ARG;
+    if (!aligned(norm, 4)) return FP8BS_ERR_ALIGN;
+    if (!workspace || workspace_bytes < fp8_grad_workspace_bytes(n)) return FP8BS_ERR_WORKSPACE;
+    if (!aligned(workspace, 8)) return FP8BS_ERR_ALIGN;
+    if (int r = check_device()) return r;
+    double* part = (double*)workspace;
+    int parts = 0;
+    const hipStream_t st = (hipStream_t)stream;
+    hipError_t e = each_table(n, g, nullptr, count, dtype, [&](const fp8bs::ClipTable& t, int grid) {
+        const hipError_t r = fp8bs::launch_grad_sumsq(t, grid, part + parts, st);
+        parts += grid;
+        return r;
+    });
+    if (e == hipSuccess) e = fp8bs::launch_grad_finish(part, parts, 0.0f, norm, nullptr, st);
+    return hip_status(e);
+}
+
+FP8BS_EXPORT int fp8_grad_clip(int64_t n, const void* const* g, const int64_t* count, const int32_t* dtype,
+                               float max_norm, void* const* out, float* norm, float* coef, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    if (int r = check_grads(n, g, count, dtype)) return r;
+    if (!(max_norm >= 0.0f) || (n > 0 && !out)) return FP8BS_ERR_ARG;
+    for (int64_t i = 0; i < n; i++)
+        if (count[i] > 0 && !out[i]) return FP8BS_ERR_ARG;
+    if (!aligned(norm, 4) || !aligned(coef, 4)) return FP8BS_ERR_ALIGN;
+    for (int64_t i = 0; i < n; i++)
+        if (!aligned(out[i], dtype[i] == FP8BS_OUT_F32 ? 4 : 2)) return FP8BS_ERR_ALIGN;
+    try {
+        if (!outputs_apart(n, g, out, count, dtype)) return FP8BS_ERR_ARG;
+    } catch (const std::bad_alloc&) {
+        return FP8BS_ERR_HIP;
+    }
+    if (!workspace || workspace_bytes < fp8_grad_workspace_bytes(n)) return FP8BS_ERR_WORKSPACE;
+    if (!aligned(workspace, 8)) return FP8BS_ERR_ALIGN;
+    if (int r = check_device()) return r;
+    double* part = (double*)workspace;
+    int parts = 0;
+    const hipStream_t st = (hipStream_t)stream;
+    hipError_t e = each_table(n, g, out, count, dtype, [&](const fp8bs::ClipTable& t, int grid) {
+        const hipError_t r = fp8bs::launch_grad_sumsq(t, grid, part + parts, st);
+        parts += grid;
+        return r;
+    });
+    if (e != hipSuccess) return hip_status(e);
+    if (parts == 0) return hip_status(fp8bs::launch_grad_finish(part, 0, max_norm, norm, coef, st));
+    e = each_table(n, g, out, count, dtype, [&](const fp8bs::ClipTable& t, int grid) {
+        return fp8bs::launch_grad_scale(t, grid, part, parts, max_norm, norm, coef, st);
+    });
+    return hip_status(e);
+}

@@ -1,0 +1,164 @@
+// clip.hip -- the global norm of many gradients, and clipping by it, for
+// gfx950.
+//
+//   norm = sqrt(sum over all tensors of g^2),  coef = min(1, max_norm / (norm + 1e-6)),
+//   out  = g * coef
+//
+// HBM-bound: every gradient read twice and written once.  Tensors come as a
+// table in the kernel's arguments, so one launch covers up to CLIP_TABLE of
+// them; workgroup w takes chunks w, w + grid, ... of all the launch's
+// elements.  Squares are summed in fp64 (an fp32 gradient's square may pass
+// fp32's range, and the sum over 1e9 elements keeps its digits); every
+// workgroup leaves one partial, and the partials are added in a fixed order,
+// so results do not depend on timing.
+#include "block_kernels.h"
+#include "device.h"
+
+namespace fp8bs {
+
+constexpr int CT = 512;
+
+// The tensor that chunk c of the launch belongs to.
+__device__ __forceinline__ int chunk_tensor(const ClipTable& t, int c) {
+    int lo = 0, hi = t.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.first[mid] <= c)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Sum over the workgroup in a fixed order; every thread gets it.
+__device__ __forceinline__ double block_sum64(double v) {
+    __shared__ double lds[CT / 64];
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+    __syncthreads();  // an earlier sum's values have been read
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int w = 0; w < CT / 64; w++) v += lds[w];
+    return v;
+}
+
+__device__ __forceinline__ double sq(float f) { return (double)f * (double)f; }
+
+__global__ __launch_bounds__(CT) void grad_sumsq_kernel(ClipTable t, double* __restrict__ part) {
+    double s = 0.0;
+    const int chunks = t.first[t.n];
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int i = chunk_tensor(t, c);
+        const int64_t at = (int64_t)(c - t.first[i]) * CLIP_CHUNK;
+        const int64_t left = t.count[i] - at;
+        const int n = (int)(left < CLIP_CHUNK ? left : CLIP_CHUNK);
+        const bool wide = ((uintptr_t)t.g[i] & 15) == 0;
+        if (t.f32[i]) {
+            const float* g = (const float*)t.g[i] + at;
+            const int n4 = wide ? n / 4 : 0;
+            for (int k = threadIdx.x; k < n4; k += CT) {
+                const float4 v = ((const float4*)g)[k];
+                s += sq(v.x) + sq(v.y) + sq(v.z) + sq(v.w);
+            }
+            for (int k = 4 * n4 + threadIdx.x; k < n; k += CT) s += sq(g[k]);
+        } else {
+            const uint16_t* g = (const uint16_t*)t.g[i] + at;
+            const int n8 = wide ? n / 8 : 0;
+            for (int k = threadIdx.x; k < n8; k += CT) {
+                const uint4 v = ((const uint4*)g)[k];
+                s += sq(bf16_lo(v.x)) + sq(bf16_hi(v.x)) + sq(bf16_lo(v.y)) + sq(bf16_hi(v.y));
+                s += sq(bf16_lo(v.z)) + sq(bf16_hi(v.z)) + sq(bf16_lo(v.w)) + sq(bf16_hi(v.w));
+            }
+            for (int k = 8 * n8 + threadIdx.x; k < n; k += CT) s += sq(bf16_lo(g[k]));
+        }
+    }
+    s = block_sum64(s);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+// norm and coefficient from the partials, the same in every workgroup.
+__device__ __forceinline__ float grad_coef(const double* __restrict__ part, int parts, float max_norm,
+                                           float* __restrict__ norm, float* __restrict__ coef) {
+    double s = 0.0;
+    for (int k = threadIdx.x; k < parts; k += CT) s += part[k];
+    s = sqrt(block_sum64(s));
+    const double c = (double)max_norm / (s + 1e-6);
+    const float f = c >= 1.0 ? 1.0f : (float)c;  // a NaN stays one
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (norm) *norm = (float)s;
+        if (coef) *coef = f;
+    }
+    return f;
+}
+
+__global__ __launch_bounds__(CT) void grad_finish_kernel(const double* part, int parts, float max_norm, float* norm,
+                                                         float* coef) {
+    grad_coef(part, parts, max_norm, norm, coef);
+}
+
+__device__ __forceinline__ uint32_t scale2(uint32_t v, float f) {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){bf16_lo(v) * f, bf16_hi(v) * f}, bf2));
+}
+
+__global__ __launch_bounds__(CT) void grad_scale_kernel(ClipTable t, const double* __restrict__ part, int parts,
+                                                        float max_norm, float* norm, float* coef) {
+    const float f = grad_coef(part, parts, max_norm, norm, coef);
+    const int chunks = t.first[t.n];
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int i = chunk_tensor(t, c);
+        if (f == 1.0f && t.out[i] == t.g[i]) continue;  // nothing to clip, in place
+        const int64_t at = (int64_t)(c - t.first[i]) * CLIP_CHUNK;
+        const int64_t left = t.count[i] - at;
+        const int n = (int)(left < CLIP_CHUNK ? left : CLIP_CHUNK);
+        const bool wide = (((uintptr_t)t.g[i] | (uintptr_t)t.out[i]) & 15) == 0;
+        if (t.f32[i]) {
+            const float* g = (const float*)t.g[i] + at;
+            float* o = (float*)t.out[i] + at;
+            const int n4 = wide ? n / 4 : 0;
+            for (int k = threadIdx.x; k < n4; k += CT) {
+                const float4 v = ((const float4*)g)[k];
+                ((float4*)o)[k] = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+            }
+            for (int k = 4 * n4 + threadIdx.x; k < n; k += CT) o[k] = g[k] * f;
+        } else {
+            const uint16_t* g = (const uint16_t*)t.g[i] + at;
+            uint16_t* o = (uint16_t*)t.out[i] + at;
+            const int n8 = wide ? n / 8 : 0;
+            for (int k = threadIdx.x; k < n8; k += CT) {
+                const uint4 v = ((const uint4*)g)[k];
+                ((uint4*)o)[k] = make_uint4(scale2(v.x, f), scale2(v.y, f), scale2(v.z, f), scale2(v.w, f));
+            }
+            for (int k = 8 * n8 + threadIdx.x; k < n; k += CT) o[k] = (uint16_t)scale2(g[k], f);
+        }
+    }
+}
+
+int clip_grid(int64_t chunks, int64_t tables) {
+    int64_t cap = 2048 / (tables > 0 ? tables : 1);
+    if (cap < 64) cap = 64;
+    return (int)(chunks < 1 ? 1 : chunks < cap ? chunks : cap);
+}
+
+hipError_t launch_grad_sumsq(const ClipTable& t, int grid, double* part, hipStream_t st) {
+    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(grid), dim3(CT), 0, st, t, part);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_finish(const double* part, int parts, float max_norm, float* norm, float* coef,
+                              hipStream_t st) {
+    hipLaunchKernelGGL(grad_finish_kernel, dim3(1), dim3(CT), 0, st, part, parts, max_norm, norm, coef);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_scale(const ClipTable& t, int grid, const double* part, int parts, float max_norm, float* norm,
+                             float* coef, hipStream_t st) {
+    hipLaunchKernelGGL(grad_scale_kernel, dim3(grid), dim3(CT), 0, st, t, part, parts, max_norm, norm, coef);
+    return hipGetLastError();
+}
+
+}  // namespace fp8bs

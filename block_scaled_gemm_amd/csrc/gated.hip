@@ -1,0 +1,873 @@
+// gated.hip -- the gated feed-forward block's kernels for gfx950.
+//
+// Forward.  H = act(G) * U with G = X Wg^T and U = X Wu^T, both from FP8
+// codes with their block scales, one launch.  Wg and Wu are stacked, [2N][K].
+// A workgroup's B tile holds the same 128 columns of both: the LDS rows are
+// dealt to the waves so that each wave multiplies WN/2 gate rows and the WN/2
+// up rows of the same columns, so a lane ends with G and U of the same
+// elements and the product is formed in its registers.  Staging, swizzle and
+// partials are those of gemm_tile.h; a K group's two block scalars (gate, up)
+// take the place of the plain tile's one or two.
+//
+// act(g) = g * sigmoid(p(g)): SiLU p = g; GELU in its tanh form
+// 0.5 g (1 + tanh(z)) = g sigmoid(2z), z = sqrt(2/pi) (g + 0.044715 g^3).
+#include "block_kernels.h"
+#include "gemm_tile.h"
+
+namespace fp8bs {
+
+// ==== activation ===========================================================================
+
+// sigmoid(p(g)), and p'(g) where DP.  exp and the reciprocal are the
+// hardware's (about one unit in the last place, and |p| * 2^-24 for exp);
+// e^-p overflowing to infinity gives 0.  GELU's cubic is taken on g clamped
+// to [-20, 20], where the sigmoid is 0 or 1 in fp32 already, so that its
+// powers stay finite.
+template <bool DP>
+__device__ __forceinline__ float gate_sigmoid(int act, float g, float& dp) {
+    float p = g;
+    if (DP) dp = 1.0f;
+    if (act != 0) {
+        const float c = __builtin_amdgcn_fmed3f(g, -20.0f, 20.0f);
+        const float k = 1.5957691216057308f;  // 2 sqrt(2/pi)
+        p = k * c * (1.0f + 0.044715f * c * c);
+        if (DP) dp = k * (1.0f + 3.0f * 0.044715f * c * c);
+    }
+    return __builtin_amdgcn_rcpf(1.0f + __expf(-p));
+}
+
+__device__ __forceinline__ float gated(int act, float g, float u) {
+    float dp;
+    return g * gate_sigmoid<false>(act, g, dp) * u;
+}
+
+// Two fp32 rounded to nearest-even bf16 and packed (v_cvt_pk_bf16_f32; a NaN
+// stays one).
+__device__ __forceinline__ uint32_t pk_bf16(float lo, float hi) {
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){lo, hi}, bf2));
+}
+
+// ==== forward: tiles =======================================================================
+//
+// All shapes hold 256 B rows: 128 gate and 128 up rows of the same columns,
+// so a row of an output tile is one 1x128 quantisation group.  Wave slot wn
+// owns LDS rows [wn*WN, (wn+1)*WN): its first half gate, its second half up,
+// of columns [wn*WN/2, (wn+1)*WN/2).
+//  Shape 20: 256 rows, waves of 64 x 128, two stages (dense FP8 modes).
+//  Shape 21: 128 rows, waves of 64 x 64, three stages (the f16 path, whose
+//    accumulators and deferred partials leave room for no more; FP8 modes
+//    with at most 128 rows).
+//  Shape 22: 64 rows, waves of 64 x 32, three stages.
+template <>
+struct Shape<20> {
+    static constexpr int BM = 256, BN = 256;
+    static constexpr int WM = 64, WN = 128;
+    static constexpr int STAGES = 2;
+    __device__ static void wave_grid(int wave, int& wm, int& wn) { Shape<0>::wave_grid(wave, wm, wn); }
+};
+template <>
+struct Shape<21> {
+    static constexpr int BM = 128, BN = 256;
+    static constexpr int WM = 64, WN = 64;
+    static constexpr int STAGES = 3;
+    // the two waves of a SIMD take the two m-slots, so 64 rows keep every SIMD busy
+    __device__ static void wave_grid(int wave, int& wm, int& wn) {
+        wm = wave >> 2;
+        wn = wave & 3;
+    }
+};
+template <>
+struct Shape<22> {
+    static constexpr int BM = 64, BN = 256;
+    static constexpr int WM = 64, WN = 32;
+    static constexpr int STAGES = 3;
+    __device__ static void wave_grid(int wave, int& wm, int& wn) {
+        wm = 0;
+        wn = wave;
+    }
+};
+
+struct GTile {
+    int64_t m0, m_end;  // rows [m0, min(m0+BM, m_end)) are real
+    int64_t n0;         // 128 output columns
+    const uint8_t* a;
+    int64_t lda;
+    const float* sa;
+    int64_t ldsa;
+    const uint8_t* bg;  // gate row n0; up row n0
+    const uint8_t* bu;
+    int64_t ldb;
+    const float* sb;   // gate block row n0/128; the up one is sb_up floats on
+    uint32_t sb_up;
+};
+
+// As Stager: per-lane source offsets fixed per tile, wave-uniform bases that
+// advance per group.  A loader issues only the A instructions whose 8-row
+// block holds a row of the tile.
+// NT: weights with the non-temporal hint (experts: each weight tile streams
+// through once).
+template <int SH, bool NT>
+struct GStager {
+    static constexpr int BM = Shape<SH>::BM, BN = Shape<SH>::BN, WN = Shape<SH>::WN;
+    static constexpr int NA = BM / 8 / LOADERS, NB = BN / 8 / LOADERS;
+    static constexpr int SA_INS = BM / 64;
+    static_assert(BN == 256 && SA_INS <= LOADERS, "one gate and one up block per tile");
+    uint32_t va[NA], vb[NB], vsa, vsb;
+    int na_valid;
+
+    // LDS row of the tile -> column, and whether it is an up row
+    __device__ static int col_of(int row) { return row / WN * (WN / 2) + row % (WN / 2); }
+    __device__ static bool is_up(int row) { return row % WN >= WN / 2; }
+
+    __device__ __forceinline__ void init(const GTile& T, int wave, int lane) {
+        const int64_t rows = T.m_end - T.m0;
+        const int64_t blocks = (rows + 7) >> 3;
+        const int64_t n = blocks > wave ? (blocks - wave + LOADERS - 1) / LOADERS : 0;
+        na_valid = (int)(n < NA ? n : NA);
+#pragma unroll
+        for (int ins = 0; ins < NA; ins++) {
+            const int row = (ins * LOADERS + wave) * 8 + (lane >> 3);
+            const int64_t m = T.m0 + row < T.m_end ? row : rows - 1;
+            va[ins] = (uint32_t)(m * T.lda) + ((((lane & 7) ^ swz(row))) << 4);
+        }
+#pragma unroll
+        for (int ins = 0; ins < NB; ins++) {
+            const int row = (ins * LOADERS + wave) * 8 + (lane >> 3);
+            vb[ins] = (uint32_t)(col_of(row) * T.ldb) + ((((lane & 7) ^ swz(row))) << 4);
+        }
+        const int64_t m = T.m0 + wave * 64 + lane < T.m_end ? wave * 64 + lane : rows - 1;
+        vsa = (uint32_t)m * 4;
+        vsb = lane == 0 ? 0 : T.sb_up * 4;  // lane 0 the gate's scalar, the others the up's
+    }
+
+    __device__ __forceinline__ void issue(const GTile& T, int64_t g, uint8_t* smem, int stage, int wave) const {
+        if (wave >= LOADERS) return;
+        const uint8_t* a = T.a + T.m0 * T.lda + g * 128;
+        const uint32_t base = lds_addr(smem + stage);
+#pragma unroll
+        for (int ins = 0; ins < NA; ins++)
+            if (ins < na_valid) dma16s(va[ins], a, base + Lds<SH>::A + (ins * LOADERS + wave) * 8 * 128);
+#pragma unroll
+        for (int ins = 0; ins < NB; ins++) {
+            const int row = (ins * LOADERS + wave) * 8;  // a block of 8 rows is all gate or all up
+            const uint8_t* b = (is_up(row) ? T.bu : T.bg) + g * 128;
+            if (NT)
+                dma16s_nt(vb[ins], b, base + Lds<SH>::B + row * 128);
+            else
+                dma16s(vb[ins], b, base + Lds<SH>::B + row * 128);
+        }
+        if (wave < SA_INS) dma4s(vsa, T.sa + g * T.ldsa + T.m0, base + Lds<SH>::SA + wave * 256);
+        if (wave == 0) dma4s(vsb, T.sb + g, base + Lds<SH>::SB);
+    }
+};
+
+// One K group on the FP8 matrix cores: as compute_mfma8 / compute_mfma8_pow2
+// with A resident, the wave's first NJ/2 fragments scaled by the gate's block
+// scalar and the others by the up's.
+template <int ACC, int SH>
+__device__ __forceinline__ void gated_group8(const uint8_t* stage, int wm, int wn, int lane, int m_valid,
+                                             v4f (&acc)[Sub<SH>::MI][Sub<SH>::NJ]) {
+    constexpr int MI = Sub<SH>::MI, NJ = Sub<SH>::NJ;
+    const uint8_t* la = stage + Lds<SH>::A;
+    const uint8_t* lb = stage + Lds<SH>::B;
+    const float* lsa = (const float*)(stage + Lds<SH>::SA);
+    const float* lsb = (const float*)(stage + Lds<SH>::SB);
+    const int mbase = wm * Shape<SH>::WM, nbase = wn * Shape<SH>::WN;
+    const int c0 = 2 * (lane >> 4);
+    if (mbase >= m_valid) return;
+    v8i af[MI];
+#pragma unroll
+    for (int i = 0; i < MI; i++) af[i] = f8_frag(la, mbase + 16 * i + (lane & 15), c0);
+    const int col = nbase + (lane & 15);
+    if constexpr (ACC == 1) {
+        if (SH == 20) offset_second_wave();
+#pragma unroll
+        for (int up = 0; up < 2; up++) {
+            float c[MI];
+            const float sbk = lsb[up];
+#pragma unroll
+            for (int i = 0; i < MI; i++) c[i] = lsa[mbase + 16 * i + (lane & 15)] * sbk;
+            if constexpr (NJ >= 4) {
+#pragma unroll
+                for (int j = up * NJ / 2; j < (up + 1) * NJ / 2; j += 2) {
+                    const v8i b0 = f8_frag(lb, col + 16 * j, c0);
+                    const v8i b1 = f8_frag(lb, col + 16 * (j + 1), c0);
+                    v4f p0[MI], p1[MI];
+#pragma unroll
+                    for (int i = 0; i < MI; i++) p0[i] = mfma8_group(b0, af[i]);
+#pragma unroll
+                    for (int i = 0; i < MI; i++) p1[i] = mfma8_group(b1, af[i]);
+#pragma unroll
+                    for (int i = 0; i < MI; i++) {
+                        acc[i][j] += p0[i] * c[i];
+                        acc[i][j + 1] += p1[i] * c[i];
+                    }
+                }
+            } else {
+                const v8i b0 = f8_frag(lb, col + 16 * up, c0);
+                v4f p0[MI];
+#pragma unroll
+                for (int i = 0; i < MI; i++) p0[i] = mfma8_group(b0, af[i]);
+#pragma unroll
+                for (int i = 0; i < MI; i++) acc[i][up] += p0[i] * c[i];
+            }
+        }
+    } else {
+        int sab[MI];
+#pragma unroll
+        for (int i = 0; i < MI; i++) sab[i] = e8m0(lsa[mbase + 16 * i + (lane & 15)]);
+        const int sbk[2] = {e8m0(lsb[0]), e8m0(lsb[1])};
+        v8i b0 = f8_frag(lb, col, c0);
+        v8i b1 = f8_frag(lb, col + 16, c0);
+#pragma unroll
+        for (int j = 0; j < NJ; j += 2) {
+            v8i n0, n1;
+            if (j + 2 < NJ) {
+                n0 = f8_frag(lb, col + 16 * (j + 2), c0);
+                n1 = f8_frag(lb, col + 16 * (j + 3), c0);
+                __builtin_amdgcn_sched_barrier(0);  // the reads stay ahead of this pair's MFMAs
+            }
+#pragma unroll
+            for (int i = 0; i < MI; i++)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b0, af[i], acc[i][j], 0, 0, 0,
+                                                                         sbk[j >= NJ / 2], 0, sab[i]);
+#pragma unroll
+            for (int i = 0; i < MI; i++)
+                acc[i][j + 1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    b1, af[i], acc[i][j + 1], 0, 0, 0, sbk[j + 1 >= NJ / 2], 0, sab[i]);
+            if (j + 2 < NJ) {
+                b0 = n0;
+                b1 = n1;
+            }
+        }
+    }
+}
+
+// One K group on the f16 matrix cores (exact widening), as
+// compute_f32_block: sub-tile j = 0 is the gate's 32 columns, j = 1 the up's,
+// and the previous group's partials p are promoted with their factors cp
+// just before their registers are reused.
+__device__ __forceinline__ void gated_group16(const uint8_t* stage, int wm, int wn, int lane, v16f (&acc)[2][2],
+                                              v16f (&p)[2][2], float (&cp)[2][2]) {
+    constexpr int SH = 21;
+    const uint8_t* la = stage + Lds<SH>::A;
+    const uint8_t* lb = stage + Lds<SH>::B;
+    const float* lsa = (const float*)(stage + Lds<SH>::SA);
+    const float* lsb = (const float*)(stage + Lds<SH>::SB);
+    const int mbase = wm * 64, nbase = wn * 64;
+    const int r = lane & 31, h = lane >> 5;
+
+    uint4 ra[2], rb[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) ra[i] = lds16(la, mbase + 32 * i + r, h);
+#pragma unroll
+    for (int j = 0; j < 2; j++) rb[j] = lds16(lb, nbase + 32 * j + r, h);
+    float cn[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const float sam = lsa[mbase + 32 * i + r];
+        cn[i][0] = sam * lsb[0];
+        cn[i][1] = sam * lsb[1];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        uint4 na[2], nb[2];
+        if (q < 3) {
+#pragma unroll
+            for (int i = 0; i < 2; i++) na[i] = lds16(la, mbase + 32 * i + r, 2 * (q + 1) + h);
+#pragma unroll
+            for (int j = 0; j < 2; j++) nb[j] = lds16(lb, nbase + 32 * j + r, 2 * (q + 1) + h);
+        }
+        v8h a0[2], a1[2], b0[2], b1[2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) widen16(ra[i], a0[i], a1[i]);
+#pragma unroll
+        for (int j = 0; j < 2; j++) widen16(rb[j], b0[j], b1[j]);
+        const v16f zero = {};
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                if (q == 0) acc[i][j] += p[i][j] * cp[i][j];
+                p[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b0[j], a0[i], q == 0 ? zero : p[i][j], 0, 0, 0);
+            }
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) p[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(b1[j], a1[i], p[i][j], 0, 0, 0);
+        if (q < 3) {
+#pragma unroll
+            for (int i = 0; i < 2; i++) ra[i] = na[i];
+#pragma unroll
+            for (int j = 0; j < 2; j++) rb[j] = nb[j];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 2; j++) cp[i][j] = cn[i][j];
+}
+
+// ==== forward: epilogue ======================================================================
+//
+// Each of G, U (where the pre-activations are kept, or the launch holds a
+// split of K) and H leaves through one 128-column fp32 image in LDS (rows of
+// 132 floats), stored in whole row segments.
+
+constexpr int GLD = 132;
+
+// Image rows to a row-major array whose column n0 is at dst.  OUT: 0 bf16, 1 fp32.
+template <int OUT>
+__device__ __forceinline__ void gated_store(const float* ep, int rows, void* dst, int64_t ld) {
+    const int t = threadIdx.x;
+    if constexpr (OUT == 1) {
+        const int c = (t & 31) * 4;
+        for (int r = t >> 5; r < rows; r += THREADS / 32)
+            *(float4*)((float*)dst + r * ld + c) = *(const float4*)&ep[r * GLD + c];
+    } else {
+        const int c = (t & 31) * 4;
+        for (int r = t >> 5; r < rows; r += THREADS / 32) {
+            const float4 v = *(const float4*)&ep[r * GLD + c];
+            *(uint2*)((uint16_t*)dst + r * ld + c) = make_uint2(pk_bf16(v.x, v.y), pk_bf16(v.z, v.w));
+        }
+    }
+}
+
+// amax of a group held four values a lane by 32 consecutive lanes.
+__device__ __forceinline__ uint32_t group32_amax(float a, float b, float c, float d) {
+    const uint32_t m = 0x7FFFFFFFu;
+    uint32_t am = max(max(__float_as_uint(a) & m, __float_as_uint(b) & m),
+                      max(__float_as_uint(c) & m, __float_as_uint(d) & m));
+    am = row16_max(am);
+    return max(am, (uint32_t)__shfl_xor((int)am, 16));
+}
+
+// Quantised H: an image row is one 1x128 group.  The scale and the codes are
+// taken from the fp32 values, one rounding (fp8_gemm_blockscaled_quant rounds
+// to bf16 between, to equal the two calls it stands for).
+__device__ __forceinline__ void gated_store_quant(const float* ep, int rows, bool pow2, uint8_t* q, int64_t ldq,
+                                                  float* qs) {
+    const int t = threadIdx.x, c = (t & 31) * 4;
+    // every lane of a 32-lane group has the same r, so a group is whole or out
+    for (int r = t >> 5; r < rows; r += THREADS / 32) {
+        const float4 v = *(const float4*)&ep[r * GLD + c];
+        const GroupScale gs = group_scale(group32_amax(v.x, v.y, v.z, v.w), pow2);
+        *(uint32_t*)(q + r * ldq + c) = pack4(v.x * gs.inv, v.y * gs.inv, v.z * gs.inv, v.w * gs.inv);
+        if (c == 0) qs[r] = gs.s;
+    }
+}
+
+// put(ep, which): the wave's values of G (0), U (1) or H (2) into the image.
+template <typename Put>
+__device__ __forceinline__ void gated_epilogue(const GatedArgs& p, const GTile& T, int BM, int64_t split,
+                                               uint8_t* smem, Put put) {
+    float* ep = (float*)smem;
+    const int rows = (int)(T.m_end - T.m0 < BM ? T.m_end - T.m0 : BM);
+    if (p.splits > 1) {
+        float* ws = p.ws + (split * p.M + T.m0) * 2 * p.N + T.n0;
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            put(ep, w);
+            __syncthreads();
+            gated_store<1>(ep, rows, ws + w * p.N, 2 * p.N);
+            __syncthreads();
+        }
+        return;
+    }
+    if (p.gu) {
+        uint16_t* gu = p.gu + T.m0 * p.ldgu + T.n0;
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            put(ep, w);
+            __syncthreads();
+            gated_store<0>(ep, rows, gu + w * p.N, p.ldgu);
+            __syncthreads();
+        }
+    }
+    put(ep, 2);
+    __syncthreads();
+    if (p.out == GATED_BF16)
+        gated_store<0>(ep, rows, (uint16_t*)p.d + T.m0 * p.ldd + T.n0, p.ldd);
+    else if (p.out == GATED_F32)
+        gated_store<1>(ep, rows, (float*)p.d + T.m0 * p.ldd + T.n0, p.ldd);
+    else
+        gated_store_quant(ep, rows, p.out == GATED_QUANT_POW2, (uint8_t*)p.d + T.m0 * p.ldd + T.n0, p.ldd,
+                          p.qs + (T.n0 >> 7) * p.qlds + T.m0);
+    __syncthreads();  // a following tile refills the stages
+}
+
+// ==== forward: one tile ======================================================================
+
+template <int ACC, int SH, bool NT>
+__device__ __forceinline__ void gated_tile(const GatedArgs& p, const GTile& T, int64_t g0, int64_t g1, int64_t split,
+                                           uint8_t* smem) {
+    constexpr int S = Shape<SH>::STAGES, BM = Shape<SH>::BM, WM = Shape<SH>::WM, WN = Shape<SH>::WN;
+    static_assert(BM * GLD * 4 <= Lds<SH>::BYTES, "the image fits in the stages");
+    static_assert(ACC != 0 || SH == 21, "the f16 path runs on 64 x 64 wave tiles");
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    int wm, wn;
+    Shape<SH>::wave_grid(wave, wm, wn);
+    const int m_valid = (int)(T.m_end - T.m0 < BM ? T.m_end - T.m0 : BM);
+
+    constexpr int MI = Sub<SH>::MI, NJ = Sub<SH>::NJ;
+    typedef typename std::conditional<ACC == 0, v16f[2][2], v4f[MI][NJ]>::type AccT;
+    AccT acc;
+    v16f pp[2][2];
+    float cp[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    if constexpr (ACC == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int r = 0; r < 16; r++) acc[i][j][r] = pp[i][j][r] = 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < MI; i++)
+#pragma unroll
+            for (int j = 0; j < NJ; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
+
+    GStager<SH, NT> stg;
+    stg.init(T, wave, lane);
+#pragma unroll
+    for (int s = 0; s < S - 1; s++)
+        if (g0 + s < g1) stg.issue(T, g0 + s, smem, s * Lds<SH>::STAGE, wave);
+    // a loader's tile loads per group; its scale loads come on top, so
+    // waiting for `per` outstanding is conservative
+    const int per = stg.na_valid + GStager<SH, NT>::NB;
+    static_assert(S == 2 || S == 3, "wait counts cover this pipeline");
+    auto step = [&](auto ss, int64_t g) {
+        constexpr int SS = decltype(ss)::value;
+        if (S == 3 && g + 1 < g1 && wave < LOADERS)
+            wait_n_and_barrier<GStager<SH, NT>::NA + GStager<SH, NT>::NB>(per);
+        else
+            wait_and_barrier<0>(wave);
+        if (g + S - 1 < g1) stg.issue(T, g + S - 1, smem, ((SS + S - 1) % S) * Lds<SH>::STAGE, wave);
+        const uint8_t* stage = smem + SS * Lds<SH>::STAGE;
+        if constexpr (ACC == 0) {
+            if (wm * 64 < m_valid) gated_group16(stage, wm, wn, lane, acc, pp, cp);
+        } else {
+            gated_group8<ACC, SH>(stage, wm, wn, lane, m_valid, acc);
+        }
+    };
+    for (int64_t g = g0; g < g1; g += S) {
+        step(std::integral_constant<int, 0>(), g);
+        if (g + 1 < g1) step(std::integral_constant<int, 1>(), g + 1);
+        if constexpr (S == 3)
+            if (g + 2 < g1) step(std::integral_constant<int, 2>(), g + 2);
+    }
+    if constexpr (ACC == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) acc[i][j] += pp[i][j] * cp[i][j];
+    }
+    wait_and_barrier<0>(wave);  // the stages hold the images next
+
+    gated_epilogue(p, T, BM, split, smem, [&](float* ep, int which) {
+        if constexpr (ACC == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float g = acc[i][0][4 * q + e], u = acc[i][1][4 * q + e];
+                        v[e] = which == 0 ? g : which == 1 ? u : gated(p.act, g, u);
+                    }
+                    *(float4*)&ep[(wm * 64 + 32 * i + (lane & 31)) * GLD + wn * 32 + 8 * q + 4 * (lane >> 5)] =
+                        make_float4(v[0], v[1], v[2], v[3]);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < MI; i++)
+#pragma unroll
+                for (int j = 0; j < NJ / 2; j++) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float g = acc[i][j][e], u = acc[i][j + NJ / 2][e];
+                        v[e] = which == 0 ? g : which == 1 ? u : gated(p.act, g, u);
+                    }
+                    *(float4*)&ep[(wm * WM + 16 * i + (lane & 15)) * GLD + wn * (WN / 2) + 16 * j +
+                                  4 * (lane >> 4)] = make_float4(v[0], v[1], v[2], v[3]);
+                }
+        }
+    });
+}
+
+__device__ __forceinline__ GTile gated_operands(const GatedArgs& p, int64_t e, int64_t n0) {
+    GTile T;
+    T.n0 = n0;
+    T.a = p.a;
+    T.lda = p.lda;
+    T.sa = p.sa;
+    T.ldsa = p.ldsa;
+    T.bg = p.b + e * p.b_estride + n0 * p.ldb;
+    T.bu = T.bg + p.N * p.ldb;
+    T.ldb = p.ldb;
+    T.sb = p.sb + e * p.sb_estride + (n0 >> 7) * p.ldsb;
+    T.sb_up = (uint32_t)((p.N >> 7) * p.ldsb);
+    return T;
+}
+
+template <int ACC, int SH>
+__global__ __launch_bounds__(THREADS) void gated_kernel(GatedArgs p, int64_t tiles_m, int64_t tiles_n) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[Lds<SH>::BYTES];
+    const int64_t ntiles = tiles_m * tiles_n;
+    const int64_t wid = xcd_remap(blockIdx.x, gridDim.x);
+    const int64_t split = wid / ntiles;
+    int64_t tm, tn;
+    tile_coords(wid % ntiles, tiles_m, tiles_n, tm, tn);
+    GTile T = gated_operands(p, 0, tn * 128);
+    T.m0 = tm * Shape<SH>::BM;
+    T.m_end = p.M;
+    const int64_t groups = p.K / 128;
+    const int64_t per = (groups + p.splits - 1) / p.splits;
+    const int64_t g0 = split * per < groups ? split * per : groups;
+    const int64_t g1 = g0 + per < groups ? g0 + per : groups;
+    gated_tile<ACC, SH, false>(p, T, g0, g1, split, smem);
+}
+
+// Experts: workgroup (expert, 128 columns) walks the expert's rows, so each
+// weight tile leaves HBM once.
+template <int ACC>
+__global__ __launch_bounds__(THREADS) void gated_grouped_kernel(GatedArgs p, int64_t tiles_n) {
+    constexpr int BYTES = ACC == 0 ? Lds<21>::BYTES : Lds<21>::BYTES > Lds<20>::BYTES ? Lds<21>::BYTES : Lds<20>::BYTES;
+    static_assert(Lds<22>::BYTES <= BYTES, "every row-tile shape fits");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[BYTES];
+    const int64_t wid = xcd_remap(blockIdx.x, gridDim.x);
+    const int64_t e = wid / tiles_n;
+    const int64_t r0 = p.offsets[e], r1 = p.offsets[e + 1];
+    GTile T = gated_operands(p, e, (wid % tiles_n) * 128);
+    T.m_end = r1;
+    const int64_t groups = p.K / 128;
+    if constexpr (ACC == 0) {
+        for (int64_t m0 = r0; m0 < r1; m0 += Shape<21>::BM) {
+            T.m0 = m0;
+            gated_tile<0, 21, true>(p, T, 0, groups, 0, smem);
+        }
+    } else {
+        for (int64_t m0 = r0; m0 < r1; m0 += Shape<20>::BM) {
+            T.m0 = m0;
+            if (r1 - m0 <= Shape<22>::BM)
+                gated_tile<ACC, 22, true>(p, T, 0, groups, 0, smem);
+            else if (r1 - m0 <= Shape<21>::BM)
+                gated_tile<ACC, 21, true>(p, T, 0, groups, 0, smem);
+            else
+                gated_tile<ACC, 20, true>(p, T, 0, groups, 0, smem);
+        }
+    }
+}
+
+// Split-K: the partials of G and U summed in split order, then the product.
+// Thread: four columns; 32 consecutive lanes hold one 1x128 group of H.
+__global__ __launch_bounds__(256) void gated_reduce_kernel(GatedArgs p) {
+    const int64_t per_row = p.N / 4;
+    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (idx >= p.M * per_row) return;  // a multiple of 32: groups are whole or out
+    const int64_t m = idx / per_row, n = idx % per_row * 4;
+    float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+    const float* w = p.ws + m * 2 * p.N + n;
+    for (int k = 0; k < p.splits; k++, w += p.M * 2 * p.N) {
+        const float4 a = *(const float4*)w, b = *(const float4*)(w + p.N);
+        g.x += a.x; g.y += a.y; g.z += a.z; g.w += a.w;
+        u.x += b.x; u.y += b.y; u.z += b.z; u.w += b.w;
+    }
+    if (p.gu) {
+        uint16_t* o = p.gu + m * p.ldgu + n;
+        *(uint2*)o = make_uint2(pk_bf16(g.x, g.y), pk_bf16(g.z, g.w));
+        *(uint2*)(o + p.N) = make_uint2(pk_bf16(u.x, u.y), pk_bf16(u.z, u.w));
+    }
+    const float h0 = gated(p.act, g.x, u.x), h1 = gated(p.act, g.y, u.y);
+    const float h2 = gated(p.act, g.z, u.z), h3 = gated(p.act, g.w, u.w);
+    if (p.out == GATED_BF16) {
+        *(uint2*)((uint16_t*)p.d + m * p.ldd + n) = make_uint2(pk_bf16(h0, h1), pk_bf16(h2, h3));
+    } else if (p.out == GATED_F32) {
+        *(float4*)((float*)p.d + m * p.ldd + n) = make_float4(h0, h1, h2, h3);
+    } else {
+        const GroupScale gs = group_scale(group32_amax(h0, h1, h2, h3), p.out == GATED_QUANT_POW2);
+        *(uint32_t*)((uint8_t*)p.d + m * p.ldd + n) = pack4(h0 * gs.inv, h1 * gs.inv, h2 * gs.inv, h3 * gs.inv);
+        if ((n & 127) == 0) p.qs[(n >> 7) * p.qlds + m] = gs.s;
+    }
+}
+
+// ==== forward: host side =====================================================================
+
+// Splits of K where the 128 x 128-column tiles would leave most CUs idle:
+// about one workgroup per CU, at least eight groups a split.
+int gated_splits(int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = ((M + 127) / 128) * (N / 128), groups = K / 128;
+    if (tiles == 0 || groups < 16 || tiles >= 128) return 1;
+    int64_t s = 256 / tiles;
+    if (s > groups / 8) s = groups / 8;
+    return s < 2 ? 1 : (int)s;
+}
+
+size_t gated_workspace(int64_t M, int64_t N, int64_t K) {
+    const int s = gated_splits(M, N, K);
+    return s <= 1 ? 0 : (size_t)s * (size_t)M * (size_t)(2 * N) * sizeof(float);
+}
+
+template <int ACC, int SH>
+static void launch_gated_shape(const GatedArgs& g, hipStream_t st) {
+    const int64_t tiles_m = (g.M + Shape<SH>::BM - 1) / Shape<SH>::BM, tiles_n = g.N / 128;
+    hipLaunchKernelGGL((gated_kernel<ACC, SH>), dim3((unsigned)(tiles_m * tiles_n * g.splits)), dim3(THREADS), 0, st,
+                       g, tiles_m, tiles_n);
+}
+
+template <int ACC>
+static void launch_gated_acc(const GatedArgs& g, hipStream_t st) {
+    if constexpr (ACC == 0) {
+        launch_gated_shape<0, 21>(g, st);
+    } else {
+        if (g.M <= Shape<22>::BM)
+            launch_gated_shape<ACC, 22>(g, st);
+        else if (g.M <= Shape<21>::BM || g.splits > 1)
+            launch_gated_shape<ACC, 21>(g, st);
+        else
+            launch_gated_shape<ACC, 20>(g, st);
+    }
+}
+
+hipError_t launch_gated(const GatedArgs& g, hipStream_t st) {
+    if (g.M == 0 || g.N == 0) return hipSuccess;
+    if (g.accum == 0)
+        launch_gated_acc<0>(g, st);
+    else if (g.accum == 1)
+        launch_gated_acc<1>(g, st);
+    else
+        launch_gated_acc<2>(g, st);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || g.splits <= 1) return e;
+    const int64_t n = g.M * (g.N / 4);
+    hipLaunchKernelGGL(gated_reduce_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, g);
+    return hipGetLastError();
+}
+
+hipError_t launch_grouped_gated(const GatedArgs& g, hipStream_t st) {
+    if (g.G == 0 || g.N == 0) return hipSuccess;
+    const int64_t tiles_n = g.N / 128;
+    const dim3 grid((unsigned)(tiles_n * g.G));
+    if (g.accum == 0)
+        hipLaunchKernelGGL(gated_grouped_kernel<0>, grid, dim3(THREADS), 0, st, g, tiles_n);
+    else if (g.accum == 1)
+        hipLaunchKernelGGL(gated_grouped_kernel<1>, grid, dim3(THREADS), 0, st, g, tiles_n);
+    else
+        hipLaunchKernelGGL(gated_grouped_kernel<2>, grid, dim3(THREADS), 0, st, g, tiles_n);
+    return hipGetLastError();
+}
+
+// ==== backward ===============================================================================
+//
+// dG = dH U act'(G), dU = dH act(G), H = act(G) U from one read of dH, G and
+// U, all in fp32 registers; dG | dU leave as 1x128 groups and, with H, as
+// 128x1 groups, each rounded once.  HBM-bound: 6 B read and 5 codes written
+// per element.
+//
+// A workgroup covers 128 rows x 128 columns.  Thread t owns rows 4(t/16) ..+3
+// and columns 8(t%16) ..+7: a load instruction reads 256 B row segments, a
+// row's 1x128 maximum is one DPP row, and the four rows of a column pack into
+// one dword of the transposed code tile.  Column maxima: registers, the wave's
+// four DPP rows, the eight waves through LDS.
+
+constexpr int BT = 512;
+
+// Max over the four 16-lane DPP rows of the wave, lane by lane (gfx950's row
+// and half-wave swaps: both results hold one of the two sides).
+__device__ __forceinline__ uint32_t rows4_max(uint32_t v) {
+    auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max((uint32_t)a[0], (uint32_t)a[1]);
+    auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max((uint32_t)b[0], (uint32_t)b[1]);
+}
+
+__device__ __forceinline__ uint32_t fabs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The rows of padded group `pg`: first row and how many of its 128 are real
+// (0: no such group).  Every expert starts a group of its own.  `found` is
+// workgroup-shared; every thread gets the answer.
+__device__ __forceinline__ void find_group(const int32_t* __restrict__ offsets, int G, int64_t pg, int64_t& row0,
+                                           int& rows) {
+    __shared__ int64_t wsum[BT / 64];
+    __shared__ int64_t found_row;
+    __shared__ int found_rows;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    if (t == 0) found_rows = 0;
+    int64_t base = 0;
+    for (int e0 = 0; e0 < G; e0 += BT) {
+        const int e = e0 + t;
+        int64_t lo = 0, n = 0;
+        if (e < G) {
+            lo = offsets[e];
+            n = (int64_t)offsets[e + 1] - lo;
+        }
+        const int64_t mine = (n + 127) / 128;
+        int64_t incl = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_up(incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 63) wsum[wave] = incl;
+        __syncthreads();
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w < BT / 64; w++) {
+            if (w < wave) incl += wsum[w];
+            total += wsum[w];
+        }
+        incl += base;
+        if (incl > pg && incl - mine <= pg) {
+            const int64_t at = (pg - (incl - mine)) * 128;
+            found_row = lo + at;
+            found_rows = (int)(n - at < 128 ? n - at : 128);
+        }
+        base += total;
+        __syncthreads();
+        if (base > pg) break;  // workgroup-uniform
+    }
+    __syncthreads();
+    row0 = found_row;
+    rows = found_rows;
+}
+
+template <bool POW2>
+__global__ __launch_bounds__(BT) void gated_bwd_kernel(GatedBwdArgs p, int64_t col_tiles) {
+    __shared__ __attribute__((aligned(16))) uint32_t codes[3 * 128 * 32];  // [tensor][column][row/4], swizzled
+    __shared__ __attribute__((aligned(16))) uint32_t wmax[3][8][128];
+    __shared__ __attribute__((aligned(16))) float inv[3][128];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int cc = t & 15, rg = t >> 4;
+    const int64_t pg = blockIdx.x / col_tiles;
+    const int64_t c0 = (blockIdx.x % col_tiles) * 128;
+    int64_t row0 = pg * 128;
+    int rows = (int)(p.M - row0 < 128 ? p.M - row0 : 128);
+    if (p.offsets) {
+        find_group(p.offsets, p.G, pg, row0, rows);
+        if (rows <= 0) return;  // workgroup-uniform: past the last group
+    }
+
+    uint4 vd[4], vg[4], vu[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int r = 4 * rg + i;
+        vd[i] = vg[i] = vu[i] = make_uint4(0, 0, 0, 0);  // rows past the end: zeros, so zero codes
+        if (r < rows) {
+            const int64_t m = row0 + r;
+            const uint16_t* g = p.gu + m * p.ldgu + c0 + 8 * cc;
+            vd[i] = *(const uint4*)(p.dh + m * p.lddh + c0 + 8 * cc);
+            vg[i] = *(const uint4*)g;
+            vu[i] = *(const uint4*)(g + p.N);
+        }
+    }
+    float x[3][4][8];  // dG, dU, H
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const uint32_t wd[4] = {vd[i].x, vd[i].y, vd[i].z, vd[i].w};
+        const uint32_t wg[4] = {vg[i].x, vg[i].y, vg[i].z, vg[i].w};
+        const uint32_t wu[4] = {vu[i].x, vu[i].y, vu[i].z, vu[i].w};
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const float d = k & 1 ? bf16_hi(wd[k / 2]) : bf16_lo(wd[k / 2]);
+            const float g = k & 1 ? bf16_hi(wg[k / 2]) : bf16_lo(wg[k / 2]);
+            const float u = k & 1 ? bf16_hi(wu[k / 2]) : bf16_lo(wu[k / 2]);
+            float dp;
+            const float s = gate_sigmoid<true>(p.act, g, dp);
+            const float a = g * s;
+            // act' = s + g s (1 - s) p'
+            x[0][i][k] = d * u * (s + a * (1.0f - s) * dp);
+            x[1][i][k] = d * a;
+            x[2][i][k] = a * u;
+        }
+    }
+
+    if (p.qr) {
+#pragma unroll
+        for (int w = 0; w < 2; w++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                uint32_t am = 0;
+#pragma unroll
+                for (int k = 0; k < 8; k++) am = max(am, fabs_bits(x[w][i][k]));
+                const GroupScale gs = group_scale(row16_max(am), POW2);
+                const int r = 4 * rg + i;
+                if (r < rows) {
+                    const float(&v)[8] = x[w][i];
+                    *(uint2*)(p.qr + (row0 + r) * p.ldqr + w * p.N + c0 + 8 * cc) =
+                        make_uint2(pack4(v[0] * gs.inv, v[1] * gs.inv, v[2] * gs.inv, v[3] * gs.inv),
+                                   pack4(v[4] * gs.inv, v[5] * gs.inv, v[6] * gs.inv, v[7] * gs.inv));
+                    if (cc == 0) p.sr[((w * p.N + c0) >> 7) * p.ldsr + row0 + r] = gs.s;
+                }
+            }
+    }
+    if (!p.qc && !p.qh) return;
+
+#pragma unroll
+    for (int w = 0; w < 3; w++) {
+        uint32_t cm[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            cm[k] = rows4_max(max(max(fabs_bits(x[w][0][k]), fabs_bits(x[w][1][k])),
+                                  max(fabs_bits(x[w][2][k]), fabs_bits(x[w][3][k]))));
+        if (lane < 16) {
+            *(uint4*)&wmax[w][wave][8 * cc] = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+            *(uint4*)&wmax[w][wave][8 * cc + 4] = make_uint4(cm[4], cm[5], cm[6], cm[7]);
+        }
+    }
+    __syncthreads();
+    if (t < 384) {
+        const int w = t >> 7, c = t & 127;
+        uint32_t am = 0;
+#pragma unroll
+        for (int k = 0; k < 8; k++) am = max(am, wmax[w][k][c]);
+        const GroupScale gs = group_scale(am, POW2);
+        inv[w][c] = gs.inv;
+        if (w == 2) {
+            if (p.qh) p.sh[pg * p.ldsh + c0 + c] = gs.s;
+        } else if (p.qc) {
+            p.sc[pg * p.ldsc + w * p.N + c0 + c] = gs.s;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 3; w++) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const float f = inv[w][8 * cc + k];
+            codes[(w * 128 + 8 * cc + k) * 32 + (rg ^ ((cc & 7) << 2))] =
+                pack4(x[w][0][k] * f, x[w][1][k] * f, x[w][2][k] * f, x[w][3][k] * f);
+        }
+    }
+    __syncthreads();
+    // 384 columns x 128 B: eight lanes write a column's run
+#pragma unroll
+    for (int k = 0; k < 6; k++) {
+        const int id = k * BT + t, c = id >> 3, ch = id & 7;
+        const int w = c >> 7, col = c & 127;
+        const uint4 v = *(const uint4*)&codes[c * 32 + ((ch ^ ((col >> 3) & 7)) << 2)];
+        if (w == 2) {
+            if (p.qh) *(uint4*)(p.qh + (c0 + col) * p.ldqh + pg * 128 + 16 * ch) = v;
+        } else if (p.qc) {
+            *(uint4*)(p.qc + (w * p.N + c0 + col) * p.ldqc + pg * 128 + 16 * ch) = v;
+        }
+    }
+}
+
+hipError_t launch_gated_backward(const GatedBwdArgs& g, hipStream_t st) {
+    const int64_t groups = (g.M + 127) / 128 + (g.offsets ? g.G : 0), col_tiles = g.N / 128;
+    if (groups == 0 || col_tiles == 0) return hipSuccess;
+    const dim3 grid((unsigned)(groups * col_tiles));
+    if (g.pow2)
+        hipLaunchKernelGGL(gated_bwd_kernel<true>, grid, dim3(BT), 0, st, g, col_tiles);
+    else
+        hipLaunchKernelGGL(gated_bwd_kernel<false>, grid, dim3(BT), 0, st, g, col_tiles);
+    return hipGetLastError();
+}
+
+}  // namespace fp8bs

@@ -116,6 +116,10 @@ enum {
     FP8BS_BSCALE_TILE = 1   /* 128x1 tiles:    SB(n,g) = sb[g*sb_s0 + n]            */
 };
 
+/* Activation of the gated products: act(g) = g * sigmoid(g) (SiLU), or GELU in
+ * its tanh form, 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))). */
+enum { FP8BS_ACT_SILU = 0, FP8BS_ACT_GELU = 1 };
+
 /* Version of this ABI (FP8BS_ABI_VERSION). */
 int fp8bs_abi_version(void);
 
@@ -478,6 +482,258 @@ int fp8_grouped_gemm_strided(int G, int64_t rows_bound, int64_t N, int64_t K,
                              int64_t sb_s1, int64_t sb_estride, void *d,
                              int64_t ldd, int out_dtype, int accum,
                              void *stream);
+
+/* ---- the gated feed-forward block ---------------------------------------- */
+
+/*
+ * fp8_gated_gemm -- both projections of a gated feed-forward layer, the
+ * activation and the product in one kernel:
+ *
+ *   G = X Wg^T,  U = X Wu^T  (block-scaled as fp8_gemm_blockscaled),
+ *   D[m][n] = act(G[m][n]) * U[m][n]
+ *
+ *   a, sa   X: codes [M][lda] and 1x128 scales sa[g*ldsa + m].
+ *   b, sb   both weights stacked, gate rows first: codes [2N][ldb] (row n
+ *           gate, row N + n up) and block scales [2N/128][ldsb] -- one
+ *           fp8_quant_block of the stacked [2N][K] weight.
+ *   act     FP8BS_ACT_SILU or FP8BS_ACT_GELU.
+ *   d       H, [M][ldd], bf16 or fp32 as out_dtype.
+ *   gu      optional (NULL = skip): the pre-activations rounded to bf16,
+ *           [M][ldgu], columns 0..N-1 G and N..2N-1 U: what
+ *           fp8_gated_backward reads ([why-be-59061], passage on caching the
+ *           activation's inputs and recomputing its output in the backward
+ *           pass).
+ *   accum   one of FP8BS_ACCUM_*.  The product is formed from the FP32
+ *           accumulators; an error of G or U enters D through act' and act.
+ *   workspace  device scratch of fp8_gated_workspace_bytes(M, N, K) bytes
+ *           (may be NULL when that is 0), for partial sums over K where there
+ *           are few rows.  Two calls that may run at the same time, two
+ *           captured graphs among them, need one each.
+ * N and K multiples of 128 (K == 0 writes zeros); M >= 0.  Values that leave
+ * the fp32 range give infinities or NaN as fp32 arithmetic does.
+ * Results do not depend on timing (sums in a fixed order).
+ * Alignment: a, b, d, gu 16-byte aligned; lda, ldb multiples of 16 (K > 0);
+ * ldd a multiple of 4, ldgu of 8; sa, sb 4-byte aligned.  lda, ldb >= K and
+ * <= FP8BS_MAX_LD; ldsa >= M; ldsb >= K/128; ldd >= N; ldgu >= 2N.
+ * Errors: ERR_ARG, ERR_SHAPE (also (N/128) * ldsb above 2^30), ERR_ALIGN,
+ * ERR_WORKSPACE, ERR_DEVICE, ERR_HIP.
+ */
+int fp8_gated_gemm(int64_t M, int64_t N, int64_t K, const uint8_t *a,
+                   int64_t lda, const float *sa, int64_t ldsa,
+                   const uint8_t *b, int64_t ldb, const float *sb,
+                   int64_t ldsb, int act, void *d, int64_t ldd, int out_dtype,
+                   uint16_t *gu, int64_t ldgu, int accum, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Workspace bytes fp8_gated_gemm and fp8_gated_gemm_quant need for this shape
+ * (0 = none). */
+size_t fp8_gated_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
+/*
+ * fp8_gated_gemm_quant -- fp8_gated_gemm with H quantised in 1x128 groups
+ * along n, ready for the down-projection: q codes [M][ldq], s[g*lds + m] the
+ * scale of row m, columns 128g .. 128g+127.  Scale and codes come from the
+ * fp32 product in one rounding (no bf16 rounding between, unlike
+ * fp8_gemm_blockscaled_quant).
+ * Alignment: q 4-byte aligned, ldq a multiple of 4; s 4-byte aligned;
+ * ldq >= N; lds >= M; otherwise as fp8_gated_gemm.
+ */
+int fp8_gated_gemm_quant(int64_t M, int64_t N, int64_t K, const uint8_t *a,
+                         int64_t lda, const float *sa, int64_t ldsa,
+                         const uint8_t *b, int64_t ldb, const float *sb,
+                         int64_t ldsb, int act, int scale_mode, uint8_t *q,
+                         int64_t ldq, float *s, int64_t lds, uint16_t *gu,
+                         int64_t ldgu, int accum, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * fp8_grouped_gated_gemm, fp8_grouped_gated_gemm_quant -- the same for a
+ * group of MoE experts: rows offsets[e] .. offsets[e+1]-1 of a (and of d, gu,
+ * q, s) belong to expert e with weights b[e] [2N][K] and scales
+ * sb[e] [2N/128][K/128], both contiguous.  offsets and rows_bound as in
+ * fp8_grouped_gemm; empty experts are allowed; rows at and after offsets[G]
+ * are neither read nor written.  No workspace.
+ */
+int fp8_grouped_gated_gemm(int G, int64_t rows_bound, int64_t N, int64_t K,
+                           const int32_t *offsets, const uint8_t *a,
+                           int64_t lda, const float *sa, int64_t ldsa,
+                           const uint8_t *b, const float *sb, int act, void *d,
+                           int64_t ldd, int out_dtype, uint16_t *gu,
+                           int64_t ldgu, int accum, void *stream);
+int fp8_grouped_gated_gemm_quant(int G, int64_t rows_bound, int64_t N,
+                                 int64_t K, const int32_t *offsets,
+                                 const uint8_t *a, int64_t lda,
+                                 const float *sa, int64_t ldsa,
+                                 const uint8_t *b, const float *sb, int act,
+                                 int scale_mode, uint8_t *q, int64_t ldq,
+                                 float *s, int64_t lds, uint16_t *gu,
+                                 int64_t ldgu, int accum, void *stream);
+
+/*
+ * fp8_gated_backward -- from dH and the kept pre-activations, everything the
+ * layer's backward GEMMs read, quantised in one pass:
+ *
+ *   dG = dH * U * act'(G),  dU = dH * act(G),  H = act(G) * U   (fp32)
+ *
+ *   dh      bf16 [M][lddh];  gu  bf16 [M][ldgu], G | U as fp8_gated_gemm.
+ *   qr, sr  dG | dU in 1x128 groups (Dgrad): codes [M][ldqr] of 2N columns,
+ *           sr[g*ldsr + m], g < 2N/128.
+ *   qc, sc  dG | dU in 128x1 groups along the rows (Wgrad of the stacked
+ *           weight): codes TRANSPOSED, [2N][ldqc], sc[p*ldsc + c], p <
+ *           ceil(M/128).
+ *   qh, sh  H in 128x1 groups (Wgrad of the down-projection): [N][ldqh],
+ *           sh[p*ldsh + c].
+ *   Each of the three outputs may be NULL (at least one is not).  A last
+ *   group of fewer than 128 rows has zero codes in its padding, so qc and qh
+ *   hold ceil(M/128)*128 rows' codes (ldqc, ldqh at least that) and the
+ *   Wgrad GEMMs run with that K.
+ * The quantised values have to be finite, as for every quantiser here.
+ * N a multiple of 128.  Alignment: dh, gu, qr, qc, qh 16-byte aligned; lddh,
+ * ldgu multiples of 8; ldqr, ldqc, ldqh of 16; scales 4-byte aligned.
+ * lddh >= N; ldgu, ldqr, ldsc >= 2N; ldsr >= M; ldsh >= N.
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_DEVICE, ERR_HIP.
+ */
+int fp8_gated_backward(int64_t M, int64_t N, const uint16_t *dh, int64_t lddh,
+                       const uint16_t *gu, int64_t ldgu, int act,
+                       int scale_mode, uint8_t *qr, int64_t ldqr, float *sr,
+                       int64_t ldsr, uint8_t *qc, int64_t ldqc, float *sc,
+                       int64_t ldsc, uint8_t *qh, int64_t ldqh, float *sh,
+                       int64_t ldsh, void *stream);
+
+/*
+ * fp8_grouped_gated_backward -- the same for the expert-sorted rows of G
+ * experts (offsets as fp8_quant_tile_grouped_col): the 128x1 groups start anew
+ * at every expert, on the padded row axis of fp8_quant_tile_grouped_col, as
+ * fp8_grouped_gemm_kgrouped reads them.  ldqc, ldqh >=
+ * fp8_grouped_col_bound(T, G); sc and sh hold that / 128 rows; bytes past the
+ * last group, and rows at and after offsets[G], are not written.
+ */
+int fp8_grouped_gated_backward(int G, const int32_t *offsets, int64_t T,
+                               int64_t N, const uint16_t *dh, int64_t lddh,
+                               const uint16_t *gu, int64_t ldgu, int act,
+                               int scale_mode, uint8_t *qr, int64_t ldqr,
+                               float *sr, int64_t ldsr, uint8_t *qc,
+                               int64_t ldqc, float *sc, int64_t ldsc,
+                               uint8_t *qh, int64_t ldqh, float *sh,
+                               int64_t ldsh, void *stream);
+
+/* ---- norms around a block -------------------------------------------------- */
+
+/*
+ * fp8_norm_residual -- the seam between two blocks in one pass over the rows:
+ *
+ *   n  = w_post ? y * r_y * w_post : y        r_y = 1/sqrt(mean(y^2) + eps)
+ *   x' = alpha * x + gate * n                 (x' = x when y is NULL)
+ *   h  = x' * r_x * w_pre                     r_x = 1/sqrt(mean(x'^2) + eps)
+ *
+ *   x        residual stream, bf16 [M][ldx].
+ *   y        optional: the block's output, bf16 [M][ldy]; needed by w_post,
+ *            gate and xo.
+ *   w_post   optional: fp32 [D], the norm after the block.
+ *   gate     optional: fp32 [ceil(M/gate_rows)][D]; row m takes gate row
+ *            m / gate_rows (a gate for each sequence; gate_rows >= M: one for
+ *            all).
+ *   xo       x', bf16 [M][ldxo] (with y).  May be x itself (same pointer and
+ *            leading dimension).
+ *   w_pre    optional: fp32 [D], the norm before the next block.  h is taken
+ *            from x' in fp32, before its rounding to xo.
+ *   h        optional: bf16 [M][ldh].
+ *   q, s     optional: h quantised in 1x128 groups, codes [M][ldq] and
+ *            s[g*lds + m] (D a multiple of 128), one rounding.
+ *   rstd_y, rstd_x  optional: r_y, r_x, fp32 [M], for the backward pass.
+ * At least one of y and w_pre is given; with w_pre at least one of h and q.
+ * D a multiple of 8, at most 32768.  eps > 0.  Quantised rows have to be
+ * finite; elsewhere infinities and NaN stay inside their row.
+ * Alignment: bf16 tensors, q and the fp32 vectors 16-byte aligned; ldx, ldy,
+ * ldxo, ldh multiples of 8, ldq of 16; s, rstd 4-byte aligned; every leading
+ * dimension >= D, lds >= M.
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_DEVICE, ERR_HIP.
+ */
+int fp8_norm_residual(int64_t M, int64_t D, const uint16_t *x, int64_t ldx,
+                      const uint16_t *y, int64_t ldy, const float *w_post,
+                      const float *gate, int64_t gate_rows, float alpha,
+                      float eps, uint16_t *xo, int64_t ldxo,
+                      const float *w_pre, uint16_t *h, int64_t ldh,
+                      int scale_mode, uint8_t *q, int64_t ldq, float *s,
+                      int64_t lds, float *rstd_y, float *rstd_x,
+                      void *stream);
+
+/*
+ * fp8_norm_residual_backward -- its gradients:
+ *
+ *   v  = dh * w_pre,  xhat = x' r_x,  yhat = y r_y, means over a row:
+ *   t  = dxo + r_x (v - xhat mean(v xhat))
+ *   dx = alpha t,  dn = gate t,  z = dn w_post
+ *   dy = r_y (z - yhat mean(z yhat))          (dn without w_post)
+ *   dw_pre = sum_m dh xhat,  dw_post = sum_m dn yhat,
+ *   dgate  = sum over a gate row's rows of t n
+ *
+ *   dxo      optional: gradient of x' from the residual stream, bf16.
+ *   dh       optional (with w_pre, xo, rstd_x, dw_pre): gradient of h, bf16.
+ *            At least one of dxo and dh is given.
+ *   xo       x' as the forward pass wrote it (x, without y).
+ *   y, w_post, gate, alpha, rstd_y   as in the forward pass.
+ *   dx, dy   bf16; dw_pre, dw_post, dgate fp32, dgate shaped as gate.  A sum
+ *            over no rows (M == 0) is zero.
+ *   workspace  fp8_norm_backward_workspace_bytes(M, D) bytes of device
+ *            scratch: the workgroups' column sums, added in a fixed order.
+ * dx may be dxo itself, and dy y itself (same pointer and leading dimension).
+ * D, alignment and leading dimensions as fp8_norm_residual (dw_pre, dw_post
+ * 4-byte, dgate 16-byte aligned).
+ * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_WORKSPACE, ERR_DEVICE, ERR_HIP.
+ */
+int fp8_norm_residual_backward(int64_t M, int64_t D, const uint16_t *dxo,
+                               int64_t lddxo, const uint16_t *dh, int64_t lddh,
+                               const uint16_t *xo, int64_t ldxo,
+                               const float *rstd_x, const float *w_pre,
+                               const uint16_t *y, int64_t ldy,
+                               const float *rstd_y, const float *w_post,
+                               const float *gate, int64_t gate_rows,
+                               float alpha, uint16_t *dx, int64_t lddx,
+                               uint16_t *dy, int64_t lddy, float *dw_pre,
+                               float *dw_post, float *dgate, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* Workspace bytes fp8_norm_residual_backward needs for this shape. */
+size_t fp8_norm_backward_workspace_bytes(int64_t M, int64_t D);
+
+/* ---- gradient norm and clipping ---------------------------------------------- */
+
+/* Largest element count of one gradient. */
+#define FP8BS_MAX_GRAD (1LL << 38)
+
+/*
+ * fp8_grad_norm -- norm[0] = sqrt(sum of g^2 over all n gradients), the
+ * squares summed in fp64 in a fixed order.
+ *   g, count, dtype   HOST arrays of n entries: device pointer, element count
+ *            (contiguous) and element type (FP8BS_OUT_BF16 or FP8BS_OUT_F32)
+ *            of each gradient.  They are read before the call returns.
+ *            Entries may be empty or alias one another; a gradient listed
+ *            twice counts twice.
+ *   workspace  fp8_grad_workspace_bytes(n) bytes of device scratch, 8-byte
+ *            aligned.
+ * fp8_grad_clip -- the same norm, and
+ *   coef[0] = min(1, max_norm / (norm + 1e-6)),  out[i] = g[i] * coef[0]
+ * with out[i] of g[i]'s type and size.  out[i] may be g[i] itself (clipping
+ * in place; not touched when coef is 1); any other overlap of an output with
+ * a gradient or another output is ERR_ARG.  norm and coef may be NULL.  A
+ * norm that is infinite gives coef 0, one that is NaN gives NaN, and the
+ * outputs are the products with it.  max_norm >= 0.
+ * Gradients are aligned to their element size; 16-byte aligned ones run
+ * faster.
+ * Errors: ERR_ARG, ERR_SHAPE (a count above FP8BS_MAX_GRAD), ERR_ALIGN,
+ * ERR_WORKSPACE, ERR_DEVICE, ERR_HIP.
+ */
+int fp8_grad_norm(int64_t n, const void *const *g, const int64_t *count,
+                  const int32_t *dtype, float *norm, void *workspace,
+                  size_t workspace_bytes, void *stream);
+int fp8_grad_clip(int64_t n, const void *const *g, const int64_t *count,
+                  const int32_t *dtype, float max_norm, void *const *out,
+                  float *norm, float *coef, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of the two calls above for n gradients. */
+size_t fp8_grad_workspace_bytes(int64_t n);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,212 @@
+"""Refusals of the feed-forward block's C ABI: bad arguments are rejected on
+the host before any HIP call (so these run without a GPU)."""
+import ctypes
+
+import pytest
+
+import block_scaled_gemm_amd as bs
+
+OK, ARG, SHAPE, ALIGN, WORKSPACE, DEVICE, HIP = range(7)
+FAKE = 1 << 20  # a 16-byte aligned non-null address that is never dereferenced
+NAN, INF = float("nan"), float("inf")
+
+
+def call(name, defaults, kw):
+    a = dict(defaults)
+    assert set(kw) <= set(a), set(kw) - set(a)
+    a.update(kw)
+    return getattr(bs.lib(), name)(*a.values(), None)
+
+
+GATED = dict(M=64, N=256, K=512, a=FAKE, lda=512, sa=FAKE, ldsa=64, b=FAKE, ldb=512, sb=FAKE, ldsb=4, act=0, d=FAKE,
+             ldd=256, out=0, gu=FAKE, ldgu=512, acc=0, ws=None, wsb=0)
+GATED_Q = dict(M=64, N=256, K=512, a=FAKE, lda=512, sa=FAKE, ldsa=64, b=FAKE, ldb=512, sb=FAKE, ldsb=4, act=0, mode=0,
+               q=FAKE, ldq=256, s=FAKE, lds=64, gu=None, ldgu=0, acc=0, ws=None, wsb=0)
+COMMON = [
+    (dict(act=2), ARG), (dict(acc=3), ARG), (dict(M=-1), ARG), (dict(a=None), ARG), (dict(sa=None), ARG),
+    (dict(b=None), ARG), (dict(sb=None), ARG), (dict(lda=256), ARG), (dict(ldb=256), ARG), (dict(ldsa=63), ARG),
+    (dict(ldsb=3), ARG), (dict(gu=FAKE, ldgu=504), ARG), (dict(K=500), SHAPE), (dict(N=200), SHAPE),
+    (dict(lda=(1 << 24) + 16), SHAPE), (dict(ldb=(1 << 24) + 16), SHAPE), (dict(ldsb=1 << 30), SHAPE),
+    (dict(a=FAKE + 8), ALIGN), (dict(b=FAKE + 8), ALIGN), (dict(sa=FAKE + 2), ALIGN), (dict(sb=FAKE + 2), ALIGN),
+    (dict(gu=FAKE + 8, ldgu=512), ALIGN), (dict(gu=FAKE, ldgu=516), ALIGN), (dict(lda=520), ALIGN),
+    (dict(ldb=520), ALIGN), (dict(M=0), OK), (dict(N=0), OK),
+    # few rows of a long K: partial sums need a workspace
+    (dict(K=8192, lda=8192, ldb=8192, ldsb=64), WORKSPACE),
+    (dict(K=8192, lda=8192, ldb=8192, ldsb=64, ws=FAKE, wsb=64), WORKSPACE),
+    (dict(K=8192, lda=8192, ldb=8192, ldsb=64, ws=FAKE + 4, wsb=1 << 30), ALIGN),
+]
+
+
+@pytest.mark.parametrize("kw,want", COMMON + [
+    (dict(out=2), ARG), (dict(d=None), ARG), (dict(ldd=128), ARG), (dict(d=FAKE + 4), ALIGN), (dict(ldd=258), ALIGN)])
+def test_gated_gemm(kw, want):
+    assert call("fp8_gated_gemm", GATED, kw) == want
+
+
+@pytest.mark.parametrize("kw,want", COMMON + [
+    (dict(mode=2), ARG), (dict(q=None), ARG), (dict(s=None), ARG), (dict(ldq=128), ARG), (dict(lds=63), ARG),
+    (dict(q=FAKE + 2), ALIGN), (dict(ldq=258), ALIGN), (dict(s=FAKE + 1), ALIGN)])
+def test_gated_gemm_quant(kw, want):
+    assert call("fp8_gated_gemm_quant", GATED_Q, kw) == want
+
+
+def test_gated_workspace_query():
+    assert bs.gated_workspace_bytes(4096, 18432, 7168) == 0
+    assert bs.gated_workspace_bytes(1, 2048, 7168) >= 2 * 4096 * 4
+    assert bs.gated_workspace_bytes(1, 100, 7168) == 0 and bs.gated_workspace_bytes(0, 2048, 7168) == 0
+
+
+GROUPED = dict(G=4, rows=64, N=256, K=512, off=FAKE, a=FAKE, lda=512, sa=FAKE, ldsa=64, b=FAKE, sb=FAKE, act=0,
+               d=FAKE, ldd=256, out=0, gu=None, ldgu=0, acc=0)
+GROUPED_Q = dict(G=4, rows=64, N=256, K=512, off=FAKE, a=FAKE, lda=512, sa=FAKE, ldsa=64, b=FAKE, sb=FAKE, act=0,
+                 mode=0, q=FAKE, ldq=256, s=FAKE, lds=64, gu=None, ldgu=0, acc=0)
+GROUPED_COMMON = [
+    (dict(G=-1), ARG), (dict(rows=-1), ARG), (dict(off=None), ARG), (dict(off=FAKE + 2), ALIGN), (dict(act=-1), ARG),
+    (dict(acc=-1), ARG), (dict(N=200), SHAPE), (dict(K=500), SHAPE), (dict(a=None), ARG), (dict(b=None), ARG),
+    (dict(lda=256), ARG), (dict(ldsa=63), ARG), (dict(gu=FAKE, ldgu=256), ARG), (dict(b=FAKE + 8), ALIGN),
+    (dict(G=0), OK), (dict(rows=0), OK), (dict(N=0), OK), (dict(G=1 << 30), SHAPE),
+]
+
+
+@pytest.mark.parametrize("kw,want", GROUPED_COMMON + [(dict(d=None), ARG), (dict(ldd=252), ARG), (dict(out=3), ARG)])
+def test_grouped_gated_gemm(kw, want):
+    assert call("fp8_grouped_gated_gemm", GROUPED, kw) == want
+
+
+@pytest.mark.parametrize("kw,want", GROUPED_COMMON + [(dict(q=None), ARG), (dict(mode=-1), ARG), (dict(lds=2), ARG)])
+def test_grouped_gated_gemm_quant(kw, want):
+    assert call("fp8_grouped_gated_gemm_quant", GROUPED_Q, kw) == want
+
+
+BWD = dict(M=200, N=256, dh=FAKE, lddh=256, gu=FAKE, ldgu=512, act=0, mode=0, qr=FAKE, ldqr=512, sr=FAKE, ldsr=200,
+           qc=FAKE, ldqc=256, sc=FAKE, ldsc=512, qh=FAKE, ldqh=256, sh=FAKE, ldsh=256)
+BWD_COMMON = [
+    (dict(act=2), ARG), (dict(mode=2), ARG), (dict(dh=None), ARG), (dict(gu=None), ARG), (dict(sr=None), ARG),
+    (dict(sc=None), ARG), (dict(sh=None), ARG), (dict(qr=None, qc=None, qh=None), ARG), (dict(N=200), SHAPE),
+    (dict(lddh=128), ARG), (dict(ldgu=256), ARG), (dict(ldqr=256), ARG), (dict(ldsr=199), ARG), (dict(ldsc=256), ARG),
+    (dict(ldsh=128), ARG), (dict(dh=FAKE + 8), ALIGN), (dict(gu=FAKE + 8), ALIGN), (dict(qr=FAKE + 8), ALIGN),
+    (dict(qc=FAKE + 8), ALIGN), (dict(qh=FAKE + 4), ALIGN), (dict(sc=FAKE + 2), ALIGN), (dict(lddh=260), ALIGN),
+    (dict(ldgu=516), ALIGN), (dict(ldqr=520), ALIGN), (dict(N=0), OK),
+]
+
+
+@pytest.mark.parametrize("kw,want", BWD_COMMON + [
+    (dict(M=-1), ARG), (dict(M=0), OK), (dict(ldqc=208), ARG), (dict(ldqh=208), ARG), (dict(ldqc=264), ALIGN)])
+def test_gated_backward(kw, want):
+    assert call("fp8_gated_backward", BWD, kw) == want
+
+
+@pytest.mark.parametrize("kw,want", BWD_COMMON + [
+    (dict(M=-1), ARG), (dict(M=0), OK), (dict(G=-1), ARG), (dict(off=None), ARG), (dict(off=FAKE + 1), ALIGN),
+    (dict(G=0), OK), (dict(ldqc=640), ARG), (dict(ldqh=640), ARG)])
+def test_grouped_gated_backward(kw, want):
+    d = dict(G=4, off=FAKE, **BWD)
+    d.update(ldqc=768, ldqh=768)
+    assert call("fp8_grouped_gated_backward", d, kw) == want
+
+
+NORM = dict(M=6, D=256, x=FAKE, ldx=256, y=FAKE, ldy=256, w_post=FAKE, gate=FAKE, gate_rows=2, alpha=1.0, eps=1e-6,
+            xo=FAKE, ldxo=256, w_pre=FAKE, h=FAKE, ldh=256, mode=0, q=FAKE, ldq=256, s=FAKE, lds=6, ry=FAKE, rx=FAKE)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(M=-1), ARG), (dict(mode=2), ARG), (dict(eps=0.0), ARG), (dict(eps=NAN), ARG), (dict(eps=INF), ARG),
+    (dict(alpha=INF), ARG), (dict(alpha=NAN), ARG), (dict(x=None), ARG), (dict(xo=None), ARG), (dict(y=None), ARG),
+    (dict(gate_rows=0), ARG), (dict(w_post=None), ARG), (dict(q=None), ARG),
+    (dict(s=None), ARG), (dict(w_pre=None), ARG), (dict(w_pre=None, h=None, q=None, s=None, rx=None, M=0), OK),
+    (dict(h=None, q=None, s=None), ARG), (dict(ldx=128), ARG), (dict(ldy=128), ARG), (dict(ldxo=128), ARG),
+    (dict(ldh=128), ARG), (dict(ldq=128), ARG), (dict(lds=5), ARG), (dict(D=252), SHAPE), (dict(D=136), SHAPE),
+    (dict(D=32896, ldx=32896, ldy=32896, ldxo=32896, ldh=32896, ldq=32896), SHAPE), (dict(x=FAKE + 8), ALIGN),
+    (dict(w_pre=FAKE + 4), ALIGN), (dict(w_post=FAKE + 4), ALIGN), (dict(gate=FAKE + 4), ALIGN),
+    (dict(q=FAKE + 8), ALIGN), (dict(ldx=260), ALIGN), (dict(ldq=264), ALIGN), (dict(rx=FAKE + 2), ALIGN),
+    (dict(M=0), OK), (dict(D=0), OK),
+])
+def test_norm(kw, want):
+    assert call("fp8_norm_residual", NORM, kw) == want
+
+
+NORM_BWD = dict(M=6, D=256, dxo=FAKE, lddxo=256, dh=FAKE, lddh=256, xo=FAKE, ldxo=256, rx=FAKE, w_pre=FAKE, y=FAKE,
+                ldy=256, ry=FAKE, w_post=FAKE, gate=FAKE, gate_rows=2, alpha=1.0, dx=FAKE, lddx=256, dy=FAKE,
+                lddy=256, dw_pre=FAKE, dw_post=FAKE, dgate=FAKE, ws=FAKE, wsb=1 << 30)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(M=-1), ARG), (dict(alpha=NAN), ARG), (dict(dxo=None, dh=None), ARG), (dict(dx=None), ARG),
+    (dict(dy=None), ARG), (dict(xo=None), ARG), (dict(rx=None), ARG), (dict(w_pre=None), ARG),
+    (dict(dw_pre=None), ARG), (dict(dw_post=None), ARG), (dict(dgate=None), ARG), (dict(ry=None), ARG),
+    (dict(y=None), ARG), (dict(gate_rows=0), ARG), (dict(D=260), SHAPE), (dict(D=32896), SHAPE),
+    (dict(lddxo=128), ARG), (dict(lddh=128), ARG), (dict(ldxo=128), ARG), (dict(ldy=128), ARG), (dict(lddx=128), ARG),
+    (dict(lddy=128), ARG), (dict(dh=FAKE + 8), ALIGN), (dict(dgate=FAKE + 4), ALIGN), (dict(dw_pre=FAKE + 2), ALIGN),
+    (dict(dh=None), ARG), (dict(w_post=None), ARG), (dict(gate=None), ARG),
+    (dict(lddx=260), ALIGN), (dict(ws=None), WORKSPACE), (dict(wsb=64), WORKSPACE), (dict(ws=FAKE + 4), ALIGN),
+    (dict(D=0), OK),
+])
+def test_norm_backward(kw, want):
+    assert call("fp8_norm_residual_backward", NORM_BWD, kw) == want
+
+
+def grads(ptrs, counts, types):
+    n = len(ptrs)
+    return (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*counts), (ctypes.c_int32 * n)(*types)
+
+
+@pytest.mark.parametrize("ptrs,counts,types,want", [
+    ([FAKE, None], [4, 4], [0, 1], ARG), ([FAKE], [-1], [0], ARG), ([FAKE], [4], [2], ARG),
+    ([FAKE + 2], [4], [1], ALIGN), ([FAKE + 1], [4], [0], ALIGN), ([FAKE], [(1 << 38) + 1], [0], SHAPE),
+])
+def test_grad_norm_and_clip(ptrs, counts, types, want):
+    p, c, t = grads(ptrs, counts, types)
+    L = bs.lib()
+    assert L.fp8_grad_norm(len(ptrs), p, c, t, FAKE, FAKE, 1 << 30, None) == want
+    assert L.fp8_grad_clip(len(ptrs), p, c, t, 1.0, p, FAKE, FAKE, FAKE, 1 << 30, None) == want
+
+
+def test_grad_clip_arguments():
+    L = bs.lib()
+    p, c, t = grads([FAKE, FAKE + 4096], [16, 16], [1, 1])
+    o, _, _ = grads([FAKE, None], [16, 16], [1, 1])
+    args = lambda **k: [{**dict(n=2, g=p, c=c, t=t, m=1.0, o=p, norm=FAKE, coef=FAKE, ws=FAKE, wsb=1 << 30), **k}[x]  # noqa: E731
+                        for x in ("n", "g", "c", "t", "m", "o", "norm", "coef", "ws", "wsb")] + [None]
+    for kw, want in ((dict(n=-1), ARG), (dict(g=None), ARG), (dict(m=-1.0), ARG), (dict(m=NAN), ARG), (dict(o=None), ARG),
+                     (dict(o=o), ARG), (dict(norm=FAKE + 2), ALIGN), (dict(coef=FAKE + 2), ALIGN),
+                     (dict(ws=None), WORKSPACE), (dict(wsb=8), WORKSPACE), (dict(ws=FAKE + 4), ALIGN)):
+        assert L.fp8_grad_clip(*args(**kw)) == want, kw
+    # overlaps: two outputs, an output in another gradient, an output shifted against its own
+    for ptrs, outs in (([FAKE, FAKE + 4096], [FAKE + 8192, FAKE + 8192 + 60]), ([FAKE, FAKE + 4096], [FAKE + 4096, FAKE]),
+                       ([FAKE, FAKE + 4096], [FAKE + 4, FAKE + 4096]), ([FAKE, FAKE], [FAKE, FAKE])):
+        g, _, _ = grads(ptrs, [16, 16], [1, 1])
+        out, _, _ = grads(outs, [16, 16], [1, 1])
+        assert L.fp8_grad_clip(*args(g=g, o=out)) == ARG, (ptrs, outs)
+    assert L.fp8_grad_norm(2, p, c, t, None, FAKE, 1 << 30, None) == ARG
+    assert L.fp8_grad_norm(2, p, c, t, FAKE, None, 0, None) == WORKSPACE
+
+
+def test_no_device_is_reported():
+    import torch
+    if torch.cuda.device_count() > 0:
+        pytest.skip("a GPU is present: this check is for GPU-less hosts")
+    assert call("fp8_gated_gemm", GATED, {}) == DEVICE
+    assert call("fp8_grouped_gated_gemm", GROUPED, {}) == DEVICE
+    assert call("fp8_gated_backward", BWD, {}) == DEVICE
+    assert call("fp8_norm_residual", NORM, {}) == DEVICE
+    assert call("fp8_norm_residual_backward", NORM_BWD, {}) == DEVICE
+    p, c, t = grads([FAKE, FAKE + 4096], [16, 16], [1, 1])
+    assert bs.lib().fp8_grad_clip(2, p, c, t, 1.0, p, FAKE, FAKE, FAKE, 1 << 30, None) == DEVICE
+    # disjoint outputs, neighbours among them, are taken
+    o, _, _ = grads([FAKE + 64, FAKE + 128], [16, 16], [1, 1])
+    assert bs.lib().fp8_grad_clip(2, p, c, t, 1.0, o, FAKE, FAKE, FAKE, 1 << 30, None) == DEVICE
+
+
+def test_cpu_tensors_are_refused():
+    import torch
+    u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
+    with pytest.raises(TypeError):
+        bs.fp8_gated_gemm(torch.zeros(2, 128, dtype=u8), torch.ones(1, 2), torch.zeros(256, 128, dtype=u8),
+                          torch.ones(2, 1))
+    with pytest.raises(TypeError):
+        bs.fp8_gated_backward(torch.zeros(2, 128, dtype=bf), torch.zeros(2, 256, dtype=bf))
+    with pytest.raises(TypeError):
+        bs.fp8_norm_residual(torch.zeros(2, 128, dtype=bf), torch.ones(128, dtype=f32))
+    for f in (bs.fp8_grad_norm, lambda g: bs.fp8_grad_clip(g, 1.0)):
+        with pytest.raises((TypeError, RuntimeError, AssertionError)):
+            f([torch.ones(3)])

@@ -1,0 +1,126 @@
+"""The global gradient norm and clipping on the GPU against 64 bits."""
+import math
+
+import pytest
+import torch
+
+import block_scaled_gemm_amd as bs
+from block_ref import F64, U32, UBF16
+
+pytestmark = pytest.mark.gpu
+
+
+def make(sizes, kinds, seed, scale=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    return [(torch.randn(n, generator=gen) * scale).to(k).cuda() for n, k in zip(sizes, kinds)]
+
+
+def expect(grads):
+    return math.sqrt(math.fsum(float(v) ** 2 for g in grads for v in g.cpu().to(F64).view(-1).norm().view(1)))
+
+
+def check(grads, before, norm, coef, max_norm):
+    total = expect(before)
+    c = min(1.0, max_norm / (total + 1e-6))
+    assert abs(float(norm) - total) <= 2 * U32 * total
+    assert abs(float(coef) - c) <= 2 * U32 * c
+    for a, b in zip(grads, before):
+        unit = U32 if a.dtype == torch.float32 else UBF16
+        w = b.cpu().to(F64) * float(coef)
+        # the product in fp32 (below its normal range, to 2^-149), and its rounding
+        off = (a.cpu().to(F64) - w).abs() - (U32 + unit) * w.abs() - 2.0 ** -133
+        assert not off.numel() or float(off.max()) <= 0
+
+
+F, B = torch.float32, torch.bfloat16
+
+
+@pytest.mark.parametrize("sizes,kinds", [
+    ([1], [F]), ([1], [B]), ([0, 5, 0], [F, B, F]), ([7, 32768, 32769, 100001], [F, F, F, F]),
+    ([7, 32768, 32769, 100001], [B, B, B, B]), ([1000, 3, 65536, 1], [F, B, B, F]), ([17] * 300, [F, B] * 150),
+    ([1 << 21], [F]), ([0], [F]), ([], []),
+])
+@pytest.mark.parametrize("max_norm", [1.0, 1e9, 0.0])
+def test_clip(hip, sizes, kinds, max_norm):
+    grads = make(sizes, kinds, len(sizes) + sum(sizes))
+    before = [g.clone() for g in grads]
+    n0 = bs.fp8_grad_norm(grads)
+    out = [torch.full_like(g, 3.0) for g in grads]
+    norm, coef = bs.fp8_grad_clip(grads, max_norm, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(grads, before)), "the gradients are read only"
+    check(out, before, norm, coef, max_norm)
+    assert torch.equal(n0, norm)
+    norm2, coef2 = bs.fp8_grad_clip(grads, max_norm)
+    assert torch.equal(norm2, norm) and torch.equal(coef2, coef)
+    assert all(torch.equal(a, b) for a, b in zip(grads, out)), "in place as into out"
+    if sum(sizes) == 0:
+        assert float(norm) == 0.0
+
+
+def test_unaligned_and_shaped(hip):
+    base = torch.randn(5000, device="cuda")
+    half = torch.randn(5001, device="cuda").bfloat16()
+    grads = [base[1:4000], base[4000:4001], half[3:4999], torch.randn(3, 5, 7, device="cuda")]
+    before = [g.clone() for g in grads]
+    guard = base[4001:].clone(), base[:1].clone(), half[:3].clone(), half[4999:].clone()
+    norm, coef = bs.fp8_grad_clip(grads, 0.5)
+    check(grads, before, norm, coef, 0.5)
+    assert torch.equal(base[4001:], guard[0]) and torch.equal(base[:1], guard[1])
+    assert torch.equal(half[:3], guard[2]) and torch.equal(half[4999:], guard[3])
+
+
+def test_beyond_fp32_squares(hip):
+    """Squares that leave fp32's range, above and below."""
+    for scale in (1e30, 1e-30):
+        g = make([4097], [F], 5, scale)
+        norm, coef = bs.fp8_grad_clip([g[0]], scale, out=[torch.empty_like(g[0])])
+        total = expect(g)
+        assert abs(float(norm) - total) <= 2 * U32 * total
+
+
+def test_non_finite(hip):
+    for bad in (float("inf"), float("nan")):
+        g = [torch.ones(300, device="cuda"), torch.ones(9, device="cuda")]
+        g[0][17] = bad
+        norm, coef = bs.fp8_grad_clip(g, 1.0)
+        if math.isinf(bad):
+            assert math.isinf(float(norm)) and float(coef) == 0.0
+            assert bool((g[1] == 0).all()) and math.isnan(float(g[0][17]))
+        else:
+            assert math.isnan(float(norm)) and math.isnan(float(coef)) and bool(torch.isnan(g[1]).all())
+
+
+def test_norm_counts_a_repeated_gradient_twice(hip):
+    g = torch.full((100,), 2.0, device="cuda")
+    assert abs(float(bs.fp8_grad_norm([g, g])) - math.sqrt(800)) < 1e-5
+
+
+def test_overlapping_outputs_are_refused(hip):
+    g = torch.ones(100, device="cuda")
+    h = torch.ones(100, device="cuda")
+    for grads, out in (([g, g], None), ([g[:60], g[40:]], None), ([g[:50], h[:50]], [h[:50], g[:50]]),
+                       ([g[:50], h[:50]], [g[10:60], h[:50]])):
+        with pytest.raises(bs.FP8BSError) as e:
+            bs.fp8_grad_clip(grads, 1.0, out=out)
+        assert e.value.status == 1
+    torch.cuda.synchronize()
+    assert bool((g == 1).all()) and bool((h == 1).all())
+
+
+def test_captured(hip):
+    grads = make([1000, 40000, 3], [F, B, F], 4)
+    out = [torch.empty_like(g) for g in grads]
+    ws = torch.empty(bs.lib().fp8_grad_workspace_bytes(3), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        norm, coef = bs.fp8_grad_clip(grads, 1.0, out=out, workspace=ws)
+    for k in range(3):
+        for g in grads:
+            g.mul_(1.5)
+        graph.replay()
+        eager = [torch.empty_like(g) for g in grads]
+        n2, c2 = bs.fp8_grad_clip(grads, 1.0, out=eager)
+        torch.cuda.synchronize()
+        assert torch.equal(norm, n2) and torch.equal(coef, c2)
+        assert all(torch.equal(a, b) for a, b in zip(out, eager))

@@ -1,0 +1,312 @@
+"""The gated feed-forward products and their backward pass on the GPU against
+the plain 64-bit forms of block_ref.py."""
+import pytest
+import torch
+
+import block_ref as ref
+import block_scaled_gemm_amd as bs
+from block_ref import F64, U32, UBF16
+
+pytestmark = pytest.mark.gpu
+
+ACCUMS = {"fp32": bs.ACCUM_FP32, "mfma8": bs.ACCUM_MFMA8, "pow2": bs.ACCUM_MFMA8_POW2}
+
+
+def make_x(M, K, pow2, seed, ld=None):
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(max(M, 1), K, generator=gen)
+    x[torch.rand(max(M, 1), K, generator=gen) < 2e-3] *= 50
+    x = x.bfloat16().cuda()
+    q, s = bs.fp8_quant_tile(x, bs.AXIS_ROW, bs.SCALE_POW2 if pow2 else bs.SCALE_FP32)
+    q, s = q[:M], s[:, :M]
+    if ld:
+        wide = torch.full((M, ld), 0x7F, dtype=torch.uint8, device="cuda")
+        wide[:, :K] = q
+        q = wide[:, :K]
+    return q, s
+
+
+def make_w(R, K, pow2, seed):
+    gen = torch.Generator().manual_seed(seed)
+    w = (torch.randn(R, K, generator=gen) * 0.05).bfloat16().cuda()
+    q, s, _ = bs.fp8_quant_block(w, bs.SCALE_POW2 if pow2 else bs.SCALE_FP32)
+    return q, s
+
+
+def bounds(g, u, sg, su, K, accum, act):
+    """Errors of G, U and the fp32 H: the accumulators', through the product
+    rule (|act'| < 1.13 for both), and the activation's own arithmetic (exp
+    of |p| <= |g| + 0.08 |g|^3 to |p| units of 2^-24, then a handful)."""
+    rel = (128 + K // 128) * U32 + (2.0 ** -10 if accum != bs.ACCUM_FP32 else 0.0)
+    eg, eu = rel * sg, rel * su
+    a = ref.act(g, act)
+    p = g.abs().clamp_max(20) if act == ref.SILU else 1.6 * (g.abs() + 0.045 * g.abs() ** 3).clamp_max(400)
+    # sigmoid's relative error, p 2^-23 + a few, falls on act(g)
+    eh = 1.13 * eg * (u.abs() + eu) + a.abs() * eu + (a * u).abs() * (8 + 2 * p) * U32
+    return eg, eu, eh + 1e-30
+
+
+def check_h(h, H, eh, dtype, tag):
+    unit = UBF16 if dtype == torch.bfloat16 else U32
+    off = (h.cpu().to(F64) - H).abs()
+    worst = float((off / (eh + unit * (H.abs() + eh) + 2.0 ** -134)).max()) if H.numel() else 0.0
+    assert worst <= 1.0, (tag, worst)
+
+
+CASES = [
+    # M, N, K: one row; a few; tile edges of 64, 128 and 256 rows; split and unsplit K
+    (1, 128, 128), (1, 256, 2048), (3, 384, 256), (63, 128, 384), (64, 256, 512), (65, 128, 640), (127, 128, 2304),
+    (128, 256, 2048), (129, 128, 256), (255, 384, 128), (257, 256, 384), (300, 1408, 512), (513, 128, 1024),
+]
+
+
+@pytest.mark.parametrize("accum", ["fp32", "mfma8", "pow2"])
+@pytest.mark.parametrize("M,N,K", CASES)
+def test_dense(hip, M, N, K, accum):
+    pow2 = accum == "pow2"
+    act = (M + N // 128) % 2
+    qx, sx = make_x(M, K, pow2, 10 * M + K)
+    qw, sw = make_w(2 * N, K, pow2, N + K)
+    H, G, U, sg, su = ref.gated(ref.rows64(qx, sx), ref.blocks64(qw, sw), act)
+    eg, eu, eh = bounds(G, U, sg, su, K, ACCUMS[accum], act)
+    h, gu = bs.fp8_gated_gemm(qx, sx, qw, sw, act, bs.OUT_BF16, save_gu=True, accum=ACCUMS[accum])
+    f, none = bs.fp8_gated_gemm(qx, sx, qw, sw, act, bs.OUT_F32, accum=ACCUMS[accum])
+    assert none is None
+    check_h(h, H, eh, torch.bfloat16, "bf16")
+    check_h(f, H, eh, torch.float32, "fp32")
+    check_h(gu[:, :N], G, eg, torch.bfloat16, "G")
+    check_h(gu[:, N:], U, eu, torch.bfloat16, "U")
+    # the bf16 H is the fp32 one rounded, bit for bit
+    assert torch.equal(h, f.bfloat16())
+    q, s, _ = bs.fp8_gated_gemm_quant(qx, sx, qw, sw, act, bs.SCALE_FP32, accum=ACCUMS[accum])
+    wq, ws = ref.quant_rows32(f)
+    assert torch.equal(q.cpu(), wq) and torch.equal(s.cpu(), ws), "quantised from the fp32 product"
+    q2, s2, gu2 = bs.fp8_gated_gemm_quant(qx, sx, qw, sw, act, bs.SCALE_POW2, save_gu=True, accum=ACCUMS[accum])
+    assert torch.equal(gu2, gu)
+    ref.check_groups(q2, s2.t(), f.cpu().to(F64), torch.zeros(M, N, dtype=F64), True, "pow2 codes")
+
+
+@pytest.mark.parametrize("accum", ["fp32", "mfma8", "pow2"])
+@pytest.mark.parametrize("sizes,N,K", [
+    ([1], 128, 128), ([0, 0, 0], 128, 256), ([0, 5, 0, 64, 65, 0], 256, 384), ([130, 1, 257, 16], 128, 512),
+    ([2] * 9, 384, 2048), ([300, 0, 17], 256, 256), ([128, 192, 256, 193], 128, 384),
+])
+def test_grouped(hip, sizes, N, K, accum):
+    pow2 = accum == "pow2"
+    G, M, tail = len(sizes), sum(sizes), 7
+    act = N // 128 % 2
+    off = torch.tensor([0] + list(torch.tensor(sizes).cumsum(0)), dtype=torch.int32, device="cuda")
+    qx, sx = make_x(M + tail, K, pow2, M + K)
+    ws = [make_w(2 * N, K, pow2, 7 * e + N) for e in range(G)]
+    qw, sw = torch.stack([w[0] for w in ws]), torch.stack([w[1] for w in ws])
+    d = torch.full((M + tail, N), 7.0, dtype=torch.float32, device="cuda")
+    gu = torch.full((M + tail, 2 * N), 7.0, dtype=torch.bfloat16, device="cuda")
+    kw = dict(accum=ACCUMS[accum])
+    bs.fp8_grouped_gated_gemm(off, qx, sx, qw, sw, act, bs.OUT_F32, d=d, gu=gu, **kw)
+    assert bool((d[M:] == 7.0).all()) and bool((gu[M:] == 7.0).all()), "rows behind the last expert are left"
+    at = 0
+    for e, n in enumerate(sizes):
+        x = ref.rows64(qx, sx)[at:at + n]
+        H, Gr, U, sg, su = ref.gated(x, ref.blocks64(qw[e], sw[e]), act)
+        eg, eu, eh = bounds(Gr, U, sg, su, K, ACCUMS[accum], act)
+        check_h(d[at:at + n], H, eh, torch.float32, f"expert {e}")
+        check_h(gu[at:at + n, :N], Gr, eg, torch.bfloat16, f"G of expert {e}")
+        check_h(gu[at:at + n, N:], U, eu, torch.bfloat16, f"U of expert {e}")
+        at += n
+    q = torch.full((M + tail, N), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.full((N // 128, M + tail), 7.0, device="cuda")
+    bs.fp8_grouped_gated_gemm_quant(off, qx, sx, qw, sw, act, bs.SCALE_FP32, q=q, s=s, **kw)
+    assert bool((q[M:] == 0x55).all()) and bool((s[:, M:] == 7.0).all())
+    if M:
+        wq, wsc = ref.quant_rows32(d[:M])
+        assert torch.equal(q[:M].cpu(), wq) and torch.equal(s[:, :M].cpu(), wsc)
+    h, _ = bs.fp8_grouped_gated_gemm(off, qx, sx, qw, sw, act, bs.OUT_BF16, **kw)
+    assert torch.equal(h[:M], d[:M].bfloat16())
+
+
+def test_strides(hip):
+    """Leading dimensions above the widths, scales of more rows than X has."""
+    M, N, K = 70, 256, 384
+    qx, sx = make_x(M, K, False, 1, ld=K + 48)
+    sx = torch.cat([sx, torch.full((K // 128, 9), float("nan"), device="cuda")], 1)
+    qw, sw = make_w(2 * N, K, False, 2)
+    wide = torch.full((2 * N, K + 16), 0x7F, dtype=torch.uint8, device="cuda")
+    wide[:, :K] = qw
+    swide = torch.full((2 * N // 128, 5), float("nan"), device="cuda")
+    swide[:, :K // 128] = sw
+    want, wgu = bs.fp8_gated_gemm(qx.contiguous(), sx[:, :M].contiguous(), qw, sw, save_gu=True)
+    d = torch.full((M, N + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    gu = torch.full((M, 2 * N + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    bs.fp8_gated_gemm(qx, sx, wide[:, :K], swide[:, :K // 128], d=d[:, :N], gu=gu[:, :2 * N])
+    assert torch.equal(d[:, :N], want) and torch.equal(gu[:, :2 * N], wgu)
+    assert bool((d[:, N:] == 3).all()) and bool((gu[:, 2 * N:] == 3).all())
+
+
+def test_extreme_gates(hip):
+    """Gates far into both tails: act is exactly g or 0, never NaN."""
+    K, N = 128, 128
+    x = torch.zeros(4, K)
+    x[:, 0] = torch.tensor([1e4, -1e4, 3e18, -3e18])
+    qx, sx = bs.fp8_quant_tile(x.bfloat16().cuda())
+    w = torch.zeros(2 * N, K)
+    w[:, 0] = 1.0
+    qw, sw, _ = bs.fp8_quant_block(w.bfloat16().cuda())
+    for act in (bs.ACT_SILU, bs.ACT_GELU):
+        for accum in (bs.ACCUM_FP32, bs.ACCUM_MFMA8):
+            h, _ = bs.fp8_gated_gemm(qx, sx, qw, sw, act, bs.OUT_F32, accum=accum)
+            h = h.cpu()
+            g = ref.rows64(qx, sx)[:, 0]
+            assert bool(torch.isfinite(h).all())
+            assert bool((h[1] == 0).all()) and bool((h[3] == 0).all())
+            for r in (0, 2):
+                off = float((h[r].double() / g[r] ** 2 - 1).abs().max())
+                # G and U are one product each; act(g) = g
+                assert off <= (2.0 ** -9 if accum == bs.ACCUM_MFMA8 else 2.0 ** -20), (act, accum, r, off)
+
+
+def test_k_zero(hip):
+    qx = torch.empty(5, 0, dtype=torch.uint8, device="cuda")
+    sx = torch.empty(0, 5, device="cuda")
+    qw, sw = torch.empty(256, 0, dtype=torch.uint8, device="cuda"), torch.empty(2, 0, device="cuda")
+    h, gu = bs.fp8_gated_gemm(qx, sx, qw, sw, save_gu=True)
+    assert bool((h == 0).all()) and bool((gu == 0).all())
+
+
+def test_repeatable_and_streams(hip):
+    """The same bits on every run, and on a stream other than the default one."""
+    M, N, K = 33, 128, 4096
+    qx, sx = make_x(M, K, False, 5)
+    qw, sw = make_w(2 * N, K, False, 6)
+    assert bs.gated_workspace_bytes(M, N, K) > 0
+    h, _ = bs.fp8_gated_gemm(qx, sx, qw, sw, accum=bs.ACCUM_MFMA8)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        h2, _ = bs.fp8_gated_gemm(qx, sx, qw, sw, accum=bs.ACCUM_MFMA8)
+    side.synchronize()
+    assert torch.equal(h, h2)
+
+
+def test_captured(hip):
+    """Two captured graphs with a workspace each, replayed in turn between
+    eager calls, give the eager results every time."""
+    N, K = 128, 2048
+    runs = []
+    for seed, M in ((1, 9), (2, 150)):
+        qx, sx = make_x(M, K, False, seed)
+        qw, sw = make_w(2 * N, K, False, seed + 5)
+        ws = torch.empty(max(1, bs.gated_workspace_bytes(M, N, K)), dtype=torch.uint8, device="cuda")
+        d = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        want, _ = bs.fp8_gated_gemm(qx, sx, qw, sw, accum=bs.ACCUM_MFMA8)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            bs.fp8_gated_gemm(qx, sx, qw, sw, d=d, workspace=ws, accum=bs.ACCUM_MFMA8)
+        runs.append((graph, d, want, (qx, sx, qw, sw, ws)))
+    for _ in range(3):
+        for _, d, _, _ in runs:
+            d.zero_()
+        for graph, _, _, _ in runs:
+            graph.replay()
+        for _, d, want, (qx, sx, qw, sw, _) in runs:
+            again, _ = bs.fp8_gated_gemm(qx, sx, qw, sw, accum=bs.ACCUM_MFMA8)
+            torch.cuda.synchronize()
+            assert torch.equal(d, want) and torch.equal(again, want)
+
+
+# ---- backward ------------------------------------------------------------------------
+
+def make_bwd(M, N, seed):
+    gen = torch.Generator().manual_seed(seed)
+    gu = (torch.randn(M, 2 * N, generator=gen) * 2).bfloat16()
+    dh = (torch.randn(M, N, generator=gen) * 1e-3).bfloat16()
+    if M and N:
+        gu[0, :4] = torch.tensor([30.0, -30.0, 0.0, -0.0]).bfloat16()
+        dh[-1] = 0
+    return dh, gu
+
+
+def bwd_bounds(dh, g, u, act):
+    """fp32 errors of dG, dU, H.  The sigmoid s and 1 - s are off by (8 +
+    2 |p|) units of s; dG = dh u (s + g s (1 - s) p') takes that on both
+    terms, and 1 - s another unit of 1."""
+    if act == ref.SILU:
+        p, dp = g.abs().clamp_max(100), torch.ones_like(g)
+    else:
+        c = g.abs().clamp_max(20)
+        p, dp = 1.6 * (c + 0.045 * c ** 3), 1.6 * (1 + 0.135 * c * c)
+    unit = (12 + 2 * p) * U32
+    a = ref.act(g, act)
+    s = torch.where(g == 0, torch.full_like(g, 0.5), a / g)
+    terms = s + a.abs() * (1 - s + unit) * dp + a.abs() * dp
+    return (dh * u).abs() * unit * terms + 1e-37, (dh * a).abs() * unit + 1e-37, (a * u).abs() * unit + 1e-37
+
+
+def check_cols(q, s, x, err, pow2, tag):
+    """Transposed codes [C, P] of x [n, C] in 128x1 groups, zero past the rows."""
+    n, C = x.shape
+    P = (n + 127) // 128 * 128
+    full, e = torch.zeros(P, C, dtype=F64), torch.zeros(P, C, dtype=F64)
+    full[:n], e[:n] = x, err
+    assert bool((q[:, n:P] == 0).all()), (tag, "padding holds zero codes")
+    ref.check_groups(q[:, :P].contiguous(), s[: P // 128].t(), full.t().contiguous(), e.t().contiguous(), pow2, tag)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("act", [ref.SILU, ref.GELU])
+@pytest.mark.parametrize("M,N", [(1, 128), (4, 256), (127, 128), (128, 384), (129, 128), (300, 256)])
+def test_backward_dense(hip, M, N, act, pow2):
+    dh, gu = make_bwd(M, N, M + N)
+    mode = bs.SCALE_POW2 if pow2 else bs.SCALE_FP32
+    out = bs.fp8_gated_backward(dh.cuda(), gu.cuda(), act, mode)
+    qr, sr, qc, sc, qh, sh = out
+    d, g, u = dh.to(F64), gu[:, :N].to(F64), gu[:, N:].to(F64)
+    dg, du, H = ref.gated_backward(d, g, u, act)
+    eg, eu, eh = bwd_bounds(d, g, u, act)
+    both, err = torch.cat([dg, du], 1), torch.cat([eg, eu], 1)
+    ref.check_groups(qr, sr.t(), both, err, pow2, "rows")
+    check_cols(qc.cpu(), sc.cpu(), both, err, pow2, "columns")
+    check_cols(qh.cpu(), sh.cpu(), H, eh, pow2, "H")
+    # switched-off outputs change nothing in the others
+    r = bs.fp8_gated_backward(dh.cuda(), gu.cuda(), act, mode, with_cols=False, with_h=False)
+    assert torch.equal(r[0], qr) and torch.equal(r[1], sr) and r[2] is r[3] is r[4] is r[5] is None
+    r = bs.fp8_gated_backward(dh.cuda(), gu.cuda(), act, mode, with_rows=False)
+    assert r[0] is None and torch.equal(r[2], qc) and torch.equal(r[4], qh) and torch.equal(r[3], sc)
+
+
+@pytest.mark.parametrize("sizes", [[5], [0, 0], [0, 1, 127, 128, 0, 129], [300, 2], [3] * 70 + [200] + [1] * 600])
+def test_backward_grouped(hip, sizes):
+    N, act, tail = 128, ref.SILU, 3
+    M, G = sum(sizes), len(sizes)
+    dh, gu = make_bwd(M + tail, N, M)
+    off = torch.tensor([0] + list(torch.tensor(sizes).cumsum(0)), dtype=torch.int32, device="cuda")
+    P = bs.grouped_col_bound(M + tail, G)
+    qc = torch.full((2 * N, P), 0x55, dtype=torch.uint8, device="cuda")
+    qh = torch.full((N, P), 0x55, dtype=torch.uint8, device="cuda")
+    sc, sh = torch.full((P // 128, 2 * N), 7.0, device="cuda"), torch.full((P // 128, N), 7.0, device="cuda")
+    qr = torch.full((M + tail, 2 * N), 0x55, dtype=torch.uint8, device="cuda")
+    sr = torch.full((2 * N // 128, M + tail), 7.0, device="cuda")
+    bs.fp8_grouped_gated_backward(off, dh.cuda(), gu.cuda(), act, qr=qr, sr=sr, qc=qc, sc=sc, qh=qh, sh=sh)
+    assert bool((qr[M:] == 0x55).all()) and bool((sr[:, M:] == 7).all()), "rows behind the last expert are left"
+    d, g, u = dh.to(F64), gu[:, :N].to(F64), gu[:, N:].to(F64)
+    dg, du, H = ref.gated_backward(d, g, u, act)
+    eg, eu, eh = bwd_bounds(d, g, u, act)
+    both, err = torch.cat([dg, du], 1), torch.cat([eg, eu], 1)
+    if M:
+        ref.check_groups(qr[:M], sr[:, :M].t(), both[:M], err[:M], False, "rows")
+    qc, qh, sc, sh = qc.cpu(), qh.cpu(), sc.cpu(), sh.cpu()
+    row = at = 0
+    for n in sizes:
+        if n:
+            e = (n + 127) // 128 * 128
+            check_cols(qc[:, at:at + e], sc[at // 128:], both[row:row + n], err[row:row + n], False, "columns")
+            check_cols(qh[:, at:at + e], sh[at // 128:], H[row:row + n], eh[row:row + n], False, "H")
+            at += e
+        row += n
+    assert bool((qc[:, at:] == 0x55).all()) and bool((sh[at // 128:] == 7).all()), "past the last group"
+    # the K-grouped quantiser of the same rows agrees on the layout: H in bf16 gives its positions
+    if M:
+        hq, _ = bs.fp8_quant_tile_grouped_col(torch.ones(M, 16, dtype=torch.bfloat16, device="cuda"), off)
+        live = hq.cpu()[0, :at] != 0
+        used = torch.cat([torch.arange((n + 127) // 128 * 128) < n for n in sizes if n])
+        assert torch.equal(live, used)

@@ -1,0 +1,239 @@
+"""The norms around a block and their backward pass on the GPU against the
+plain 64-bit forms of block_ref.py."""
+import pytest
+import torch
+
+import block_ref as ref
+import block_scaled_gemm_amd as bs
+from block_ref import F64, U32, UBF16
+
+pytestmark = pytest.mark.gpu
+
+# rounding of a row's sum: up to 32 serial adds in a lane, 6 in the wave, 16
+# over the waves, and a handful of products
+SUM = 64 * U32
+
+
+def make(M, D, post, gated, gate_rows, seed):
+    gen = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    B = -(-M // gate_rows) if M else 0
+    return dict(x=rnd(M, D).bfloat16(), y=(3 * rnd(M, D)).bfloat16(), w_pre=1 + 0.3 * rnd(D),
+                w_post=1 + 0.3 * rnd(D) if post else None, gate=rnd(B, D) if gated else None,
+                dxo=rnd(M, D).bfloat16(), dh=rnd(M, D).bfloat16())
+
+
+def up(t):
+    return None if t is None else t.to(F64)
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+def near(got, want, err, unit, tag):
+    off = (got.cpu().to(F64) - want).abs()
+    worst = float((off / (err + unit * (want.abs() + err) + 1e-37)).max()) if off.numel() else 0.0
+    assert worst <= 1.0, (tag, worst)
+
+
+def forward_bounds(c, xo, h, rx, gate, alpha, y, ry):
+    """fp32 errors of x', h and the relative one of r_x."""
+    n = y if c["w_post"] is None else y * ry[:, None] * up(c["w_post"])
+    ex = 2 * SUM * ((alpha * up(c["x"])).abs() + (n if gate is None else gate * n).abs())
+    rel = SUM + ex.norm(dim=1) / xo.norm(dim=1).clamp_min(1e-30)
+    eh = up(c["w_pre"]).abs() * rx[:, None] * ex + h.abs() * (rel[:, None] + 4 * U32)
+    return ex, eh, rel
+
+
+CASES = [
+    # M, D, gate rows: one row; few columns; odd widths; every vector count; gates that cross workgroups or not
+    (1, 128, 1), (1, 7168, 1), (3, 256, 2), (5, 2048, 100), (33, 384, 7), (64, 1024, 64), (130, 8192, 129),
+    (17, 8320, 4), (9, 16384, 9), (4, 20480, 2), (2, 32768, 1), (700, 128, 1), (1500, 256, 13), (1025, 128, 600),
+]
+
+
+@pytest.mark.parametrize("post,gated,alpha", [(True, True, 1.0), (True, False, 0.5), (False, True, -1.25),
+                                              (False, False, 1.0)])
+@pytest.mark.parametrize("M,D,rows", CASES)
+def test_forward(hip, M, D, rows, post, gated, alpha):
+    c = make(M, D, post, gated, rows, M + D)
+    gate = ref.gate_rows_of(up(c["gate"]), rows, M) if gated else None
+    xo, h, ry, rx = ref.norm(up(c["x"]), up(c["y"]), up(c["w_post"]), gate, alpha, up(c["w_pre"]))
+    ex, eh, rel = forward_bounds(c, xo, h, rx, gate, alpha, up(c["y"]), ry)
+    kw = dict(y=dev(c["y"]), w_post=dev(c["w_post"]), gate=dev(c["gate"]), gate_rows=rows if gated else None,
+              alpha=alpha)
+    r = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), want_h=True, **kw)
+    near(r.xo, xo, ex, UBF16, "x'")
+    near(r.h, h, eh, UBF16, "h")
+    near(r.rstd_x, rx, rel * rx, U32, "r_x")
+    if post:
+        near(r.rstd_y, ry, SUM * ry, U32, "r_y")
+    else:
+        assert r.rstd_y is None
+    ref.check_groups(r.q, r.s.t(), h, eh, False, "codes")
+    p = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), scale_mode=bs.SCALE_POW2, **kw)
+    ref.check_groups(p.q, p.s.t(), h, eh, True, "pow2 codes")
+    assert p.h is None and torch.equal(p.xo, r.xo)
+    # without the next norm, in place
+    x = dev(c["x"]).clone()
+    n = bs.fp8_norm_residual(x, None, xo=x, **kw)
+    assert n.h is n.q is n.s is n.rstd_x is None and torch.equal(x, r.xo)
+
+
+@pytest.mark.parametrize("M,D", [(1, 8), (2, 24), (5, 136), (3, 128), (40, 520)])
+def test_pre_norm_alone(hip, M, D):
+    c = make(M, D, False, False, 1, D)
+    _, h, _, rx = ref.norm(up(c["x"]), w_pre=up(c["w_pre"]))
+    r = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), quantise=D % 128 == 0, want_h=True)
+    near(r.h, h, 2 * SUM * h.abs(), UBF16, "h")
+    near(r.rstd_x, rx, SUM * rx, U32, "r_x")
+    assert r.xo is None and r.rstd_y is None and (r.q is None) == (D % 128 != 0)
+
+
+def test_zero_and_infinite_rows(hip):
+    """A zero row gives zeros; an infinity or NaN stays in its row."""
+    M, D = 6, 256
+    c = make(M, D, True, False, 1, 9)
+    x, y = c["x"].clone(), c["y"].clone()
+    x[1] = 0
+    y[1] = 0
+    x[3, 5] = float("inf")
+    y[4, 7] = float("nan")
+    kw = dict(w_post=dev(c["w_post"]), quantise=False, want_h=True)
+    r = bs.fp8_norm_residual(dev(x), dev(c["w_pre"]), y=dev(y), **kw)
+    assert bool((r.h[1] == 0).all()) and bool((r.xo[1] == 0).all())
+    assert not bool(torch.isfinite(r.h[3]).all()) and bool(torch.isnan(r.h[4]).any())
+    clean = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), y=dev(c["y"]), **kw)
+    for m in (0, 2, 5):
+        assert torch.equal(r.h[m], clean.h[m]) and torch.equal(r.xo[m], clean.xo[m])
+
+
+def test_strides(hip):
+    M, D = 11, 384
+    c = make(M, D, True, True, 4, 5)
+    wide = lambda t, fill: torch.cat([t, torch.full((M, 8), fill, dtype=t.dtype)], 1).cuda()[:, :D]  # noqa: E731
+    kw = dict(w_post=dev(c["w_post"]), gate=dev(c["gate"]), gate_rows=4)
+    want = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), y=dev(c["y"]), want_h=True, **kw)
+    nan = float("nan")
+    xo, h = torch.full((M, D + 8), 5.0).bfloat16().cuda(), torch.full((M, D + 16), 5.0).bfloat16().cuda()
+    q = torch.full((M, D + 16), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.full((D // 128, M + 3), 5.0, device="cuda")
+    bs.fp8_norm_residual(wide(c["x"], nan), dev(c["w_pre"]), y=wide(c["y"], nan), xo=xo[:, :D], h=h[:, :D], q=q[:, :D],
+                         s=s, **kw)
+    assert torch.equal(xo[:, :D], want.xo) and torch.equal(h[:, :D], want.h) and torch.equal(q[:, :D], want.q)
+    assert torch.equal(s[:, :M], want.s) and bool((s[:, M:] == 5).all()) and bool((q[:, D:] == 0x55).all())
+    assert bool((xo[:, D:] == 5).all()) and bool((h[:, D:] == 5).all())
+
+
+def backward_checks(c, M, D, rows, post, gated, alpha, with_dxo, with_dh, r, xo, rx, ry):
+    d = {k: up(v) for k, v in c.items()}
+    dxo, dh = d["dxo"] if with_dxo else None, d["dh"] if with_dh else None
+    args = (xo, rx, d["w_pre"], d["y"], ry, d["w_post"], d["gate"], rows, alpha)
+    dx, dy, dw_pre, dw_post, dgate = ref.norm_backward(dxo, dh, *args)
+    # sizes of what is added up, for the bounds: the same formulas on magnitudes
+    t0 = torch.zeros(M, D, dtype=F64) if dxo is None else dxo.abs()
+    t = t0
+    xh = xo.abs() * rx[:, None] if with_dh else torch.zeros(M, D, dtype=F64)
+    mean_v = torch.zeros(M, 1, dtype=F64)
+    if with_dh:
+        v = (dh * d["w_pre"]).abs()
+        mean_v = (v * xh).mean(1, keepdim=True)
+        t = t0 + rx[:, None] * (v + xh * mean_v)
+    et = 2 * SUM * t
+    yh = d["y"].abs() * (ry[:, None] if post else 1.0)
+    n = yh * d["w_post"].abs() if post else yh
+    g = ref.gate_rows_of(d["gate"], rows, M).abs() if gated else torch.ones(M, D, dtype=F64)
+    edy = 2 * et * g + 4 * SUM * t * g
+    if post:
+        wp = d["w_post"].abs()
+        z = t * g * wp
+        # the row mean is off by a sum's rounding and by that of t, both on magnitudes
+        edy = ry[:, None] * (4 * SUM * z + yh * 6 * SUM * (z * yh).mean(1, keepdim=True))
+    near(r.dx, dx, abs(alpha) * et, UBF16, "dx")
+    near(r.dy, dy, edy, UBF16, "dy")
+    # column sums: serial over a workgroup's rows, then over the workgroups
+    col = (-(-M // 512) + 64) * U32 + 4 * SUM
+    if with_dh:
+        near(r.dw_pre, dw_pre, col * (dh.abs() * xh).sum(0), U32, "dw_pre")
+    if post:
+        near(r.dw_post, dw_post, col * (t * g * yh).sum(0), U32, "dw_post")
+    if gated:
+        size = torch.zeros_like(d["gate"]).index_add_(0, torch.arange(M) // rows, t * n)
+        near(r.dgate, dgate, col * size, U32, "dgate")
+
+
+@pytest.mark.parametrize("post,gated,alpha", [(True, True, 1.0), (True, False, 0.5), (False, True, -1.25),
+                                              (False, False, 1.0)])
+@pytest.mark.parametrize("M,D,rows", CASES)
+def test_backward(hip, M, D, rows, post, gated, alpha):
+    c = make(M, D, post, gated, rows, M + D + 1)
+    kw = dict(y=dev(c["y"]), w_post=dev(c["w_post"]), gate=dev(c["gate"]), gate_rows=rows if gated else None,
+              alpha=alpha)
+    f = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), **kw)
+    xo, rx = up(f.xo.cpu()), up(f.rstd_x.cpu())
+    ry = up(f.rstd_y.cpu()) if post else None
+    for with_dxo, with_dh in ((True, True), (True, False), (False, True)):
+        r = bs.fp8_norm_residual_backward(dev(c["dxo"]) if with_dxo else None, dev(c["dh"]) if with_dh else None,
+                                          f.xo, f.rstd_x, dev(c["w_pre"]), rstd_y=f.rstd_y, **kw)
+        assert (r.dw_pre is None) == (not with_dh) and (r.dw_post is None) == (not post)
+        backward_checks(c, M, D, rows, post, gated, alpha, with_dxo, with_dh, r, xo, rx, ry)
+    # in place: dx over dxo, dy over y
+    dxo, y = dev(c["dxo"]).clone(), dev(c["y"]).clone()
+    kw["y"] = y
+    r2 = bs.fp8_norm_residual_backward(dxo, dev(c["dh"]), f.xo, f.rstd_x, dev(c["w_pre"]), rstd_y=f.rstd_y, dx=dxo,
+                                       dy=y, **kw)
+    kw["y"] = dev(c["y"])
+    r = bs.fp8_norm_residual_backward(dev(c["dxo"]), dev(c["dh"]), f.xo, f.rstd_x, dev(c["w_pre"]), rstd_y=f.rstd_y,
+                                      **kw)
+    assert torch.equal(r2.dx, r.dx) and torch.equal(r2.dy, r.dy) and torch.equal(r2.dw_pre, r.dw_pre)
+    for a, b in ((r2.dw_post, r.dw_post), (r2.dgate, r.dgate)):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
+def test_pre_norm_backward_and_no_rows(hip):
+    M, D = 7, 264
+    c = make(M, D, False, False, 1, 3)
+    f = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), quantise=False, want_h=True)
+    r = bs.fp8_norm_residual_backward(dev(c["dxo"]), dev(c["dh"]), dev(c["x"]), f.rstd_x, dev(c["w_pre"]))
+    rx = up(f.rstd_x.cpu())
+    dx, _, dw, _, _ = ref.norm_backward(up(c["dxo"]), up(c["dh"]), up(c["x"]), rx, up(c["w_pre"]), None, None, None,
+                                        None, 1, 1.0)
+    size = up(c["dxo"]).abs() + rx[:, None] * (up(c["dh"]) * up(c["w_pre"])).abs() * 8
+    near(r.dx, dx, 2 * SUM * size, UBF16, "dx")
+    near(r.dw_pre, dw, 4 * SUM * (up(c["dh"]) * up(c["x"]) * rx[:, None]).abs().sum(0), U32, "dw_pre")
+    assert r.dy is None and r.dw_post is None and r.dgate is None
+    e = torch.empty(0, D, dtype=torch.bfloat16, device="cuda")
+    r = bs.fp8_norm_residual_backward(e, e, e, torch.empty(0, device="cuda"), dev(c["w_pre"]))
+    assert r.dx.shape == (0, D) and bool((r.dw_pre == 0).all())
+    w, g = dev(c["w_pre"]), torch.empty(0, D, device="cuda")
+    r = bs.fp8_norm_residual_backward(e, e, e, torch.empty(0, device="cuda"), w, y=e, rstd_y=torch.empty(0, device="cuda"),
+                                      w_post=w, gate=g, gate_rows=3)
+    assert bool((r.dw_pre == 0).all()) and bool((r.dw_post == 0).all()) and r.dgate.shape == (0, D)
+    assert bs.fp8_norm_residual(e, w, y=e, w_post=w, quantise=False, want_h=True).h.shape == (0, D)
+
+
+def test_captured(hip):
+    M, D = 300, 256
+    c = make(M, D, True, True, 70, 8)
+    x, y, w_pre, w_post, gate = (dev(c[k]) for k in ("x", "y", "w_pre", "w_post", "gate"))
+    kw = dict(y=y, w_post=w_post, gate=gate, gate_rows=70)
+
+    def step():
+        f = bs.fp8_norm_residual(x, w_pre, **kw)
+        g = bs.fp8_norm_residual_backward(dev_dxo, dev_dh, f.xo, f.rstd_x, w_pre, rstd_y=f.rstd_y, **kw)
+        return (f.xo, f.q, f.s) + tuple(g)
+    dev_dxo, dev_dh = dev(c["dxo"]), dev(c["dh"])
+    want = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        again = step()
+        torch.cuda.synchronize()
+        for a, b, e in zip(got, want, again):
+            assert torch.equal(a, b) and torch.equal(e, b)
