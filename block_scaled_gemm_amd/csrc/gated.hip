@@ -18,22 +18,26 @@ namespace fp8bs {
 
 // ==== activation ===========================================================================
 
-// sigmoid(p(g)), and p'(g) where DP.  exp and the reciprocal are the
-// hardware's (about one unit in the last place, and |p| * 2^-24 for exp);
-// e^-p overflowing to infinity gives 0.  GELU's cubic is taken on g clamped
-// to [-20, 20], where the sigmoid is 0 or 1 in fp32 already, so that its
-// powers stay finite.
+// sigmoid(p(g)), and p'(g) where DP, to a few units in the last place: e^-p as
+// 2^t with the rounding error of t = -p log2(e) put back as a factor, then
+// the hardware's reciprocal.  g is clamped where the sigmoid is 0 or 1 in fp32
+// already (|p| = 104: e^p overflows to infinity, whose reciprocal is 0; 20
+// for GELU), so that every step stays finite or goes to the right end.
 template <bool DP>
 __device__ __forceinline__ float gate_sigmoid(int act, float g, float& dp) {
-    float p = g;
+    float p = __builtin_amdgcn_fmed3f(g, -104.0f, 104.0f);
     if (DP) dp = 1.0f;
     if (act != 0) {
         const float c = __builtin_amdgcn_fmed3f(g, -20.0f, 20.0f);
         const float k = 1.5957691216057308f;  // 2 sqrt(2/pi)
-        p = k * c * (1.0f + 0.044715f * c * c);
+        p = __builtin_amdgcn_fmed3f(k * c * (1.0f + 0.044715f * c * c), -104.0f, 104.0f);
         if (DP) dp = k * (1.0f + 3.0f * 0.044715f * c * c);
     }
-    return __builtin_amdgcn_rcpf(1.0f + __expf(-p));
+    const float l2e = 1.44269504088896f, rest = 1.92596299e-8f;  // log2(e) = l2e + rest
+    const float t = -p * l2e;
+    const float r = __builtin_fmaf(-p, l2e, -t) - p * rest;
+    const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(r, 0.693147181f, 1.0f);
+    return __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 __device__ __forceinline__ float gated(int act, float g, float u) {
@@ -104,8 +108,10 @@ struct GTile {
 };
 
 // As Stager: per-lane source offsets fixed per tile, wave-uniform bases that
-// advance per group.  A loader issues only the A instructions whose 8-row
-// block holds a row of the tile.
+// advance per group.  A loader's B rows all lie a wave-uniform distance from
+// its first ones, so one per-lane offset serves them (eight registers fewer,
+// which the 64 x 128 wave tile does not have).  On the shorter tiles a loader
+// issues only the A instructions whose 8-row block holds a row of the tile.
 // NT: weights with the non-temporal hint (experts: each weight tile streams
 // through once).
 template <int SH, bool NT>
@@ -113,30 +119,33 @@ struct GStager {
     static constexpr int BM = Shape<SH>::BM, BN = Shape<SH>::BN, WN = Shape<SH>::WN;
     static constexpr int NA = BM / 8 / LOADERS, NB = BN / 8 / LOADERS;
     static constexpr int SA_INS = BM / 64;
+    static constexpr bool SKIP = BM < 256;
     static_assert(BN == 256 && SA_INS <= LOADERS, "one gate and one up block per tile");
-    uint32_t va[NA], vb[NB], vsa, vsb;
+    uint32_t va[NA], vb, vsa, vsb;
     int na_valid;
 
-    // LDS row of the tile -> column, and whether it is an up row
+    // LDS row of the tile -> column, and whether it is an up row; a block of
+    // 8 rows is all gate or all up, its columns consecutive
     __device__ static int col_of(int row) { return row / WN * (WN / 2) + row % (WN / 2); }
     __device__ static bool is_up(int row) { return row % WN >= WN / 2; }
 
     __device__ __forceinline__ void init(const GTile& T, int wave, int lane) {
         const int64_t rows = T.m_end - T.m0;
-        const int64_t blocks = (rows + 7) >> 3;
-        const int64_t n = blocks > wave ? (blocks - wave + LOADERS - 1) / LOADERS : 0;
-        na_valid = (int)(n < NA ? n : NA);
+        if (SKIP) {
+            const int64_t blocks = (rows + 7) >> 3;
+            const int64_t n = blocks > wave ? (blocks - wave + LOADERS - 1) / LOADERS : 0;
+            na_valid = (int)(n < NA ? n : NA);
+        } else {
+            na_valid = NA;
+        }
 #pragma unroll
         for (int ins = 0; ins < NA; ins++) {
             const int row = (ins * LOADERS + wave) * 8 + (lane >> 3);
             const int64_t m = T.m0 + row < T.m_end ? row : rows - 1;
             va[ins] = (uint32_t)(m * T.lda) + ((((lane & 7) ^ swz(row))) << 4);
         }
-#pragma unroll
-        for (int ins = 0; ins < NB; ins++) {
-            const int row = (ins * LOADERS + wave) * 8 + (lane >> 3);
-            vb[ins] = (uint32_t)(col_of(row) * T.ldb) + ((((lane & 7) ^ swz(row))) << 4);
-        }
+        // rows 32 apart share the swizzle
+        vb = (uint32_t)((lane >> 3) * T.ldb) + ((((lane & 7) ^ swz(wave * 8 + (lane >> 3)))) << 4);
         const int64_t m = T.m0 + wave * 64 + lane < T.m_end ? wave * 64 + lane : rows - 1;
         vsa = (uint32_t)m * 4;
         vsb = lane == 0 ? 0 : T.sb_up * 4;  // lane 0 the gate's scalar, the others the up's
@@ -148,15 +157,15 @@ struct GStager {
         const uint32_t base = lds_addr(smem + stage);
 #pragma unroll
         for (int ins = 0; ins < NA; ins++)
-            if (ins < na_valid) dma16s(va[ins], a, base + Lds<SH>::A + (ins * LOADERS + wave) * 8 * 128);
+            if (!SKIP || ins < na_valid) dma16s(va[ins], a, base + Lds<SH>::A + (ins * LOADERS + wave) * 8 * 128);
 #pragma unroll
         for (int ins = 0; ins < NB; ins++) {
-            const int row = (ins * LOADERS + wave) * 8;  // a block of 8 rows is all gate or all up
-            const uint8_t* b = (is_up(row) ? T.bu : T.bg) + g * 128;
+            const int row = (ins * LOADERS + wave) * 8;
+            const uint8_t* b = (is_up(row) ? T.bu : T.bg) + col_of(row) * T.ldb + g * 128;
             if (NT)
-                dma16s_nt(vb[ins], b, base + Lds<SH>::B + row * 128);
+                dma16s_nt(vb, b, base + Lds<SH>::B + row * 128);
             else
-                dma16s(vb[ins], b, base + Lds<SH>::B + row * 128);
+                dma16s(vb, b, base + Lds<SH>::B + row * 128);
         }
         if (wave < SA_INS) dma4s(vsa, T.sa + g * T.ldsa + T.m0, base + Lds<SH>::SA + wave * 256);
         if (wave == 0) dma4s(vsb, T.sb + g, base + Lds<SH>::SB);
@@ -167,7 +176,7 @@ struct GStager {
 // with A resident, the wave's first NJ/2 fragments scaled by the gate's block
 // scalar and the others by the up's.
 template <int ACC, int SH>
-__device__ __forceinline__ void gated_group8(const uint8_t* stage, int wm, int wn, int lane, int m_valid,
+__device__ __forceinline__ void gated_group8(const uint8_t* stage, int wm, int wn, int lane,
                                              v4f (&acc)[Sub<SH>::MI][Sub<SH>::NJ]) {
     constexpr int MI = Sub<SH>::MI, NJ = Sub<SH>::NJ;
     const uint8_t* la = stage + Lds<SH>::A;
@@ -176,7 +185,9 @@ __device__ __forceinline__ void gated_group8(const uint8_t* stage, int wm, int w
     const float* lsb = (const float*)(stage + Lds<SH>::SB);
     const int mbase = wm * Shape<SH>::WM, nbase = wn * Shape<SH>::WN;
     const int c0 = 2 * (lane >> 4);
-    if (mbase >= m_valid) return;
+    // a wave whose rows are all past the end multiplies them all the same:
+    // leaving here made the compiler merge the accumulators at every group
+    // and spill (4096 x 18432 x 7168: 7.3 ms)
     v8i af[MI];
 #pragma unroll
     for (int i = 0; i < MI; i++) af[i] = f8_frag(la, mbase + 16 * i + (lane & 15), c0);
@@ -451,7 +462,7 @@ __device__ __forceinline__ void gated_tile(const GatedArgs& p, const GTile& T, i
         if constexpr (ACC == 0) {
             if (wm * 64 < m_valid) gated_group16(stage, wm, wn, lane, acc, pp, cp);
         } else {
-            gated_group8<ACC, SH>(stage, wm, wn, lane, m_valid, acc);
+            gated_group8<ACC, SH>(stage, wm, wn, lane, acc);
         }
     };
     for (int64_t g = g0; g < g1; g += S) {
