@@ -359,7 +359,7 @@ FP8BS_EXPORT int fp8_norm_residual_backward(int64_t M, int64_t D, const uint16_t
     g.dw_post = dw_post;
     g.dgate = dgate;
     g.ws = (float*)workspace;
-    g.parts = fp8bs::norm_bwd_parts(M);
+    g.parts = fp8bs::norm_bwd_parts(M, D);
     return hip_status(fp8bs::launch_norm_bwd(g, (hipStream_t)stream));
 }
 

@@ -131,7 +131,7 @@ struct NormBwdArgs {
     int parts;
 };
 
-int norm_bwd_parts(int64_t M);
+int norm_bwd_parts(int64_t M, int64_t D);
 size_t norm_bwd_workspace(int64_t M, int64_t D);
 hipError_t launch_norm_bwd(const NormBwdArgs& g, hipStream_t st);
 

@@ -24,7 +24,7 @@ namespace fp8bs {
 // already (|p| = 104: e^p overflows to infinity, whose reciprocal is 0; 20
 // for GELU), so that every step stays finite or goes to the right end.
 template <bool DP>
-__device__ __forceinline__ float gate_sigmoid(int act, float g, float& dp) {
+__device__ __forceinline__ float gate_sigmoid(const int act, float g, float& dp) {
     float p = __builtin_amdgcn_fmed3f(g, -104.0f, 104.0f);
     if (DP) dp = 1.0f;
     if (act != 0) {
@@ -685,20 +685,46 @@ hipError_t launch_grouped_gated(const GatedArgs& g, hipStream_t st) {
 // and columns 8(t%16) ..+7: a load instruction reads 256 B row segments, a
 // row's 1x128 maximum is one DPP row, and the four rows of a column pack into
 // one dword of the transposed code tile.  Column maxima: registers, the wave's
-// four DPP rows, the eight waves through LDS.
+// four DPP rows, the eight waves through LDS.  The tile's three fp32 tensors are
+// 192 KB, so three quarters of H wait in LDS for the column maxima: at 128
+// registers a thread and 78 KB, two workgroups share a CU and one's loads
+// overlap the other's arithmetic.
 
 constexpr int BT = 512;
 
-// Max over the four 16-lane DPP rows of the wave, lane by lane (gfx950's row
-// and half-wave swaps: both results hold one of the two sides).
-__device__ __forceinline__ uint32_t rows4_max(uint32_t v) {
+// Max over the four 16-lane DPP rows of the wave, lane by lane, of values >= 0
+// (gfx950's row and half-wave swaps: both results hold one of the two sides).
+__device__ __forceinline__ float rows4_max(float f) {
+    uint32_t v = __float_as_uint(f);
     auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
     v = max((uint32_t)a[0], (uint32_t)a[1]);
     auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return max((uint32_t)b[0], (uint32_t)b[1]);
+    return __uint_as_float(max((uint32_t)b[0], (uint32_t)b[1]));
 }
 
-__device__ __forceinline__ uint32_t fabs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+__device__ __forceinline__ float amax2(float a, float b) { return fmaxf(fabsf(a), fabsf(b)); }
+
+// Four codes of values already within a group's range (|y| <= 448 up to the
+// product's rounding, which the conversion takes back to 448), packed.
+__device__ __forceinline__ uint32_t pack4_scaled(float y0, float y1, float y2, float y3) {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y0, y1, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y2, y3, lo, true);
+}
+
+// Every input is read once and every code written once: the loads and the
+// row codes are non-temporal (4096 x 18432: 200 -> 190 us), the column codes'
+// 16-byte stores, eight of which make a line, are not.
+typedef uint32_t u32x4_s __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_s __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
+    const u32x4_s v = __builtin_nontemporal_load((const u32x4_s*)p);
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+__device__ __forceinline__ void st_stream8(uint8_t* p, uint32_t lo, uint32_t hi) {
+    __builtin_nontemporal_store((u32x2_s){lo, hi}, (u32x2_s*)p);
+}
 
 // The rows of padded group `pg`: first row and how many of its 128 are real
 // (0: no such group).  Every expert starts a group of its own.  `found` is
@@ -748,15 +774,17 @@ __device__ __forceinline__ void find_group(const int32_t* __restrict__ offsets, 
     rows = found_rows;
 }
 
-template <bool POW2>
-__global__ __launch_bounds__(BT) void gated_bwd_kernel(GatedBwdArgs p, int64_t col_tiles) {
-    __shared__ __attribute__((aligned(16))) uint32_t codes[3 * 128 * 32];  // [tensor][column][row/4], swizzled
-    __shared__ __attribute__((aligned(16))) uint32_t wmax[3][8][128];
+template <bool POW2, int ACT>
+__global__ __launch_bounds__(BT) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_kernel(
+    GatedBwdArgs p, int64_t col_tiles) {
+    __shared__ __attribute__((aligned(16))) uint32_t codes[128 * 32];  // [column][row/4], swizzled
+    __shared__ __attribute__((aligned(16))) float4 hs[6][BT];          // H of three of a thread's rows
+    __shared__ __attribute__((aligned(16))) float wmax[3][8][128];
     __shared__ __attribute__((aligned(16))) float inv[3][128];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int cc = t & 15, rg = t >> 4;
-    const int64_t pg = blockIdx.x / col_tiles;
-    const int64_t c0 = (blockIdx.x % col_tiles) * 128;
+    const int64_t pg = blockIdx.x / col_tiles, ct = blockIdx.x % col_tiles;
+    const int64_t c0 = ct * 128;
     int64_t row0 = pg * 128;
     int rows = (int)(p.M - row0 < 128 ? p.M - row0 : 128);
     if (p.offsets) {
@@ -767,17 +795,21 @@ __global__ __launch_bounds__(BT) void gated_bwd_kernel(GatedBwdArgs p, int64_t c
     uint4 vd[4], vg[4], vu[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const int r = 4 * rg + i;
-        vd[i] = vg[i] = vu[i] = make_uint4(0, 0, 0, 0);  // rows past the end: zeros, so zero codes
-        if (r < rows) {
-            const int64_t m = row0 + r;
-            const uint16_t* g = p.gu + m * p.ldgu + c0 + 8 * cc;
-            vd[i] = *(const uint4*)(p.dh + m * p.lddh + c0 + 8 * cc);
-            vg[i] = *(const uint4*)g;
-            vu[i] = *(const uint4*)(g + p.N);
-        }
+        const int r = 4 * rg + i < rows ? 4 * rg + i : rows - 1;
+        const uint16_t* d = p.dh + (row0 + r) * p.lddh + c0 + 8 * cc;
+        const uint16_t* g = p.gu + (row0 + r) * p.ldgu + c0 + 8 * cc;
+        vd[i] = ld_stream(d);
+        vg[i] = ld_stream(g);
+        vu[i] = ld_stream(g + p.N);
     }
-    float x[3][4][8];  // dG, dU, H
+    if (rows < 128) {  // rows past the end: zeros, so zero codes
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (4 * rg + i >= rows) vd[i] = vg[i] = vu[i] = make_uint4(0, 0, 0, 0);
+    }
+    float x[2][4][8], h[8], hm[8];  // dG, dU; H of this row; column maxima of H
+#pragma unroll
+    for (int k = 0; k < 8; k++) hm[k] = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const uint32_t wd[4] = {vd[i].x, vd[i].y, vd[i].z, vd[i].w};
@@ -789,55 +821,57 @@ __global__ __launch_bounds__(BT) void gated_bwd_kernel(GatedBwdArgs p, int64_t c
             const float g = k & 1 ? bf16_hi(wg[k / 2]) : bf16_lo(wg[k / 2]);
             const float u = k & 1 ? bf16_hi(wu[k / 2]) : bf16_lo(wu[k / 2]);
             float dp;
-            const float s = gate_sigmoid<true>(p.act, g, dp);
+            const float s = gate_sigmoid<true>(ACT, g, dp);
             const float a = g * s;
             // act' = s + g s (1 - s) p'
             x[0][i][k] = d * u * (s + a * (1.0f - s) * dp);
             x[1][i][k] = d * a;
-            x[2][i][k] = a * u;
+            h[k] = a * u;
+            hm[k] = fmaxf(hm[k], fabsf(h[k]));
         }
-    }
-
-    if (p.qr) {
+        if (i < 3) {
+            hs[2 * i][t] = make_float4(h[0], h[1], h[2], h[3]);
+            hs[2 * i + 1][t] = make_float4(h[4], h[5], h[6], h[7]);
+        }
+        if (p.qr) {
+            const int r = 4 * rg + i;
 #pragma unroll
-        for (int w = 0; w < 2; w++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                uint32_t am = 0;
-#pragma unroll
-                for (int k = 0; k < 8; k++) am = max(am, fabs_bits(x[w][i][k]));
-                const GroupScale gs = group_scale(row16_max(am), POW2);
-                const int r = 4 * rg + i;
+            for (int w = 0; w < 2; w++) {
+                const float(&v)[8] = x[w][i];
+                const float am = fmaxf(fmaxf(amax2(v[0], v[1]), amax2(v[2], v[3])),
+                                       fmaxf(amax2(v[4], v[5]), amax2(v[6], v[7])));
+                const GroupScale gs = group_scale(row16_max(__float_as_uint(am)), POW2);
                 if (r < rows) {
-                    const float(&v)[8] = x[w][i];
-                    *(uint2*)(p.qr + (row0 + r) * p.ldqr + w * p.N + c0 + 8 * cc) =
-                        make_uint2(pack4(v[0] * gs.inv, v[1] * gs.inv, v[2] * gs.inv, v[3] * gs.inv),
-                                   pack4(v[4] * gs.inv, v[5] * gs.inv, v[6] * gs.inv, v[7] * gs.inv));
+                    st_stream8(p.qr + (row0 + r) * p.ldqr + w * p.N + c0 + 8 * cc,
+                               pack4_scaled(v[0] * gs.inv, v[1] * gs.inv, v[2] * gs.inv, v[3] * gs.inv),
+                               pack4_scaled(v[4] * gs.inv, v[5] * gs.inv, v[6] * gs.inv, v[7] * gs.inv));
                     if (cc == 0) p.sr[((w * p.N + c0) >> 7) * p.ldsr + row0 + r] = gs.s;
                 }
             }
+        }
+        // one row at a time: with the rows mixed the compiler spills
+        __builtin_amdgcn_sched_barrier(0);
     }
     if (!p.qc && !p.qh) return;
 
 #pragma unroll
     for (int w = 0; w < 3; w++) {
-        uint32_t cm[8];
+        float cm[8];
 #pragma unroll
         for (int k = 0; k < 8; k++)
-            cm[k] = rows4_max(max(max(fabs_bits(x[w][0][k]), fabs_bits(x[w][1][k])),
-                                  max(fabs_bits(x[w][2][k]), fabs_bits(x[w][3][k]))));
+            cm[k] = rows4_max(w == 2 ? hm[k] : fmaxf(amax2(x[w][0][k], x[w][1][k]), amax2(x[w][2][k], x[w][3][k])));
         if (lane < 16) {
-            *(uint4*)&wmax[w][wave][8 * cc] = make_uint4(cm[0], cm[1], cm[2], cm[3]);
-            *(uint4*)&wmax[w][wave][8 * cc + 4] = make_uint4(cm[4], cm[5], cm[6], cm[7]);
+            *(float4*)&wmax[w][wave][8 * cc] = make_float4(cm[0], cm[1], cm[2], cm[3]);
+            *(float4*)&wmax[w][wave][8 * cc + 4] = make_float4(cm[4], cm[5], cm[6], cm[7]);
         }
     }
     __syncthreads();
     if (t < 384) {
         const int w = t >> 7, c = t & 127;
-        uint32_t am = 0;
+        float am = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; k++) am = max(am, wmax[w][k][c]);
-        const GroupScale gs = group_scale(am, POW2);
+        for (int k = 0; k < 8; k++) am = fmaxf(am, wmax[w][k][c]);
+        const GroupScale gs = group_scale(__float_as_uint(am), POW2);
         inv[w][c] = gs.inv;
         if (w == 2) {
             if (p.qh) p.sh[pg * p.ldsh + c0 + c] = gs.s;
@@ -846,28 +880,45 @@ __global__ __launch_bounds__(BT) void gated_bwd_kernel(GatedBwdArgs p, int64_t c
         }
     }
     __syncthreads();
+    // one tensor's codes at a time through the 16 KB tile
 #pragma unroll
     for (int w = 0; w < 3; w++) {
+        uint8_t* q = w == 2 ? p.qh + c0 * p.ldqh : p.qc + (w * p.N + c0) * p.ldqc;
+        const int64_t ldq = w == 2 ? p.ldqh : p.ldqc;
+        if (w == 2 ? !p.qh : !p.qc) continue;  // workgroup-uniform
+        float v[3][8];
+        if (w == 2) {
+#pragma unroll
+            for (int i = 0; i < 3; i++) {
+                *(float4*)&v[i][0] = hs[2 * i][t];
+                *(float4*)&v[i][4] = hs[2 * i + 1][t];
+            }
+        }
 #pragma unroll
         for (int k = 0; k < 8; k++) {
             const float f = inv[w][8 * cc + k];
-            codes[(w * 128 + 8 * cc + k) * 32 + (rg ^ ((cc & 7) << 2))] =
-                pack4(x[w][0][k] * f, x[w][1][k] * f, x[w][2][k] * f, x[w][3][k] * f);
+            codes[(8 * cc + k) * 32 + (rg ^ ((cc & 7) << 2))] =
+                w == 2 ? pack4_scaled(v[0][k] * f, v[1][k] * f, v[2][k] * f, h[k] * f)
+                       : pack4_scaled(x[w & 1][0][k] * f, x[w & 1][1][k] * f, x[w & 1][2][k] * f, x[w & 1][3][k] * f);
         }
-    }
-    __syncthreads();
-    // 384 columns x 128 B: eight lanes write a column's run
+        __syncthreads();
+        // 128 columns x 128 B: eight lanes write a column's run
 #pragma unroll
-    for (int k = 0; k < 6; k++) {
-        const int id = k * BT + t, c = id >> 3, ch = id & 7;
-        const int w = c >> 7, col = c & 127;
-        const uint4 v = *(const uint4*)&codes[c * 32 + ((ch ^ ((col >> 3) & 7)) << 2)];
-        if (w == 2) {
-            if (p.qh) *(uint4*)(p.qh + (c0 + col) * p.ldqh + pg * 128 + 16 * ch) = v;
-        } else if (p.qc) {
-            *(uint4*)(p.qc + (w * p.N + c0 + col) * p.ldqc + pg * 128 + 16 * ch) = v;
+        for (int k = 0; k < 2; k++) {
+            const int id = k * BT + t, col = id >> 3, ch = id & 7;
+            *(uint4*)(q + col * ldq + pg * 128 + 16 * ch) =
+                *(const uint4*)&codes[col * 32 + ((ch ^ ((col >> 3) & 7)) << 2)];
         }
+        __syncthreads();
     }
+}
+
+template <bool POW2>
+static void launch_bwd(const GatedBwdArgs& g, const dim3 grid, int64_t col_tiles, hipStream_t st) {
+    if (g.act == 0)
+        hipLaunchKernelGGL((gated_bwd_kernel<POW2, 0>), grid, dim3(BT), 0, st, g, col_tiles);
+    else
+        hipLaunchKernelGGL((gated_bwd_kernel<POW2, 1>), grid, dim3(BT), 0, st, g, col_tiles);
 }
 
 hipError_t launch_gated_backward(const GatedBwdArgs& g, hipStream_t st) {
@@ -875,9 +926,9 @@ hipError_t launch_gated_backward(const GatedBwdArgs& g, hipStream_t st) {
     if (groups == 0 || col_tiles == 0) return hipSuccess;
     const dim3 grid((unsigned)(groups * col_tiles));
     if (g.pow2)
-        hipLaunchKernelGGL(gated_bwd_kernel<true>, grid, dim3(BT), 0, st, g, col_tiles);
+        launch_bwd<true>(g, grid, col_tiles, st);
     else
-        hipLaunchKernelGGL(gated_bwd_kernel<false>, grid, dim3(BT), 0, st, g, col_tiles);
+        launch_bwd<false>(g, grid, col_tiles, st);
     return hipGetLastError();
 }
 

@@ -22,21 +22,10 @@ __device__ __forceinline__ uint32_t pk_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){lo, hi}, bf2));
 }
 
-// Eight bf16 (zeros where !on) widened to fp32.
-__device__ __forceinline__ void load8(const uint16_t* p, bool on, float (&v)[8]) {
-    const uint4 w = on ? *(const uint4*)p : make_uint4(0, 0, 0, 0);
-    v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-    v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
-}
-
 __device__ __forceinline__ void loadf8(const float* p, bool on, float (&v)[8]) {
     const float4 a = on ? *(const float4*)p : make_float4(0, 0, 0, 0);
     const float4 b = on ? *(const float4*)(p + 4) : make_float4(0, 0, 0, 0);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
-    *(uint4*)p = make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -65,37 +54,82 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*lds)[16][N], in
     slot ^= 1;
 }
 
-// Thread t owns columns 8(t + j*threads) ..+7, j < NV.
-template <int NV>
-__global__ __launch_bounds__(1024) void norm_kernel(NormArgs p, int64_t rows_per) {
+// Rows stream through once, so their loads and stores are non-temporal (norm
+// of 8192 x 7168: 108 -> 104 us).  raw8: eight bf16 as loaded; widening them is
+// put off so that the next row's wait in half the registers.
+typedef uint32_t u32x4_n __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_n __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint4 raw8(const uint16_t* p, bool on) {
+    u32x4_n v = {0, 0, 0, 0};
+    if (on) v = __builtin_nontemporal_load((const u32x4_n*)p);
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+__device__ __forceinline__ void widen8(const uint4& w, float (&v)[8]) {
+    v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+    v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+    const u32x4_n w = {pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7])};
+    __builtin_nontemporal_store(w, (u32x4_n*)p);
+}
+
+constexpr int NORM_ROWS = 16;  // most rows of a workgroup
+
+// Thread t owns columns 8(t + j*threads) ..+7, j < NV.  The next row is loaded
+// before this one's sums.  gw holds gate * w_post (or the one there is).
+template <int NV, int MAXT>
+__global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs p, int64_t rows_per) {
     __shared__ float red[2][16][1];
+    // the rows' scales leave together: a group's are neighbours in memory
+    __shared__ float scales[NORM_ROWS][NORM_MAX_COLS / 128 + 1];
     int slot = 0;
     const int t = threadIdx.x, nt = blockDim.x;
     const int64_t r0 = blockIdx.x * rows_per, r1 = r0 + rows_per < p.M ? r0 + rows_per : p.M;
     const float inv_d = 1.0f / (float)p.D;
+    const bool scaled = p.gate || p.w_post;
     int64_t col[NV];
     bool on[NV];
-    float wpre[NV][8], wpost[NV][8], gate[NV][8];
+    float wpre[NV][8], gw[NV][8];
+    uint4 nx[NV], ny[NV];
 #pragma unroll
     for (int j = 0; j < NV; j++) {
         col[j] = 8 * (int64_t)(t + j * nt);
         on[j] = col[j] < p.D;
+        nx[j] = raw8(p.x + r0 * p.ldx + col[j], on[j]);
+        if (p.y) ny[j] = raw8(p.y + r0 * p.ldy + col[j], on[j]);
         if (p.w_pre) loadf8(p.w_pre + col[j], on[j], wpre[j]);
-        if (p.w_post) loadf8(p.w_post + col[j], on[j], wpost[j]);
+        if (p.w_post && !p.gate) loadf8(p.w_post + col[j], on[j], gw[j]);
     }
-    int64_t have = -1;  // the row of `gate` in registers
+    int64_t next_gate = p.gate ? r0 / p.gate_rows * p.gate_rows : p.M;  // first row of the next gate row
     for (int64_t r = r0; r < r1; r++) {
         float x[NV][8], y[NV][8];
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            load8(p.x + r * p.ldx + col[j], on[j], x[j]);
-            if (p.y) load8(p.y + r * p.ldy + col[j], on[j], y[j]);
+            widen8(nx[j], x[j]);
+            if (p.y) widen8(ny[j], y[j]);
+        }
+        if (r + 1 < r1) {
+#pragma unroll
+            for (int j = 0; j < NV; j++) {
+                nx[j] = raw8(p.x + (r + 1) * p.ldx + col[j], on[j]);
+                if (p.y) ny[j] = raw8(p.y + (r + 1) * p.ldy + col[j], on[j]);
+            }
         }
         if (p.y) {
-            if (p.gate && r / p.gate_rows != have) {
-                have = r / p.gate_rows;
+            if (r >= next_gate) {
 #pragma unroll
-                for (int j = 0; j < NV; j++) loadf8(p.gate + have * p.D + col[j], on[j], gate[j]);
+                for (int j = 0; j < NV; j++) {
+                    loadf8(p.gate + next_gate / p.gate_rows * p.D + col[j], on[j], gw[j]);
+                    if (p.w_post) {
+                        float w[8];
+                        loadf8(p.w_post + col[j], on[j], w);
+#pragma unroll
+                        for (int k = 0; k < 8; k++) gw[j][k] *= w[k];
+                    }
+                }
+                next_gate += p.gate_rows;
             }
             float ry = 1.0f;
             if (p.w_post) {
@@ -112,10 +146,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p, int64_t rows_per
             for (int j = 0; j < NV; j++) {
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
-                    float n = y[j][k];
-                    if (p.w_post) n = n * ry * wpost[j][k];
-                    if (p.gate) n *= gate[j][k];
-                    x[j][k] = p.alpha * x[j][k] + n;
+                    const float n = y[j][k] * ry;
+                    x[j][k] = p.alpha * x[j][k] + (scaled ? n * gw[j][k] : n);
                 }
                 if (on[j]) store8(p.xo + r * p.ldxo + col[j], x[j]);
             }
@@ -132,41 +164,55 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p, int64_t rows_per
         if (t == 0 && p.rstd_x) p.rstd_x[r] = rx;
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            float h[8];
-            uint32_t am = 0;
+            float h[8], am = 0.f;
 #pragma unroll
             for (int k = 0; k < 8; k++) {
                 h[k] = x[j][k] * rx * wpre[j][k];
-                am = max(am, __float_as_uint(h[k]) & 0x7FFFFFFFu);
+                am = fmaxf(am, fabsf(h[k]));
             }
             if (p.q) {
                 // 16 lanes hold a group; lanes past D are whole groups
-                const GroupScale gs = group_scale(row16_max(am), p.pow2);
+                const GroupScale gs = group_scale(row16_max(__float_as_uint(am)), p.pow2);
                 if (on[j]) {
-                    *(uint2*)(p.q + r * p.ldq + col[j]) =
-                        make_uint2(pack4(h[0] * gs.inv, h[1] * gs.inv, h[2] * gs.inv, h[3] * gs.inv),
-                                   pack4(h[4] * gs.inv, h[5] * gs.inv, h[6] * gs.inv, h[7] * gs.inv));
-                    if ((t & 15) == 0) p.s[(col[j] >> 7) * p.lds + r] = gs.s;
+                    const u32x2_n c = {pack4(h[0] * gs.inv, h[1] * gs.inv, h[2] * gs.inv, h[3] * gs.inv),
+                                       pack4(h[4] * gs.inv, h[5] * gs.inv, h[6] * gs.inv, h[7] * gs.inv)};
+                    __builtin_nontemporal_store(c, (u32x2_n*)(p.q + r * p.ldq + col[j]));
+                    if ((t & 15) == 0) scales[r - r0][col[j] >> 7] = gs.s;
                 }
             }
             if (p.h && on[j]) store8(p.h + r * p.ldh + col[j], h);
         }
     }
+    if (!p.q) return;
+    __syncthreads();
+    const int rows = (int)(r1 - r0), groups = (int)(p.D >> 7);
+    for (int i = t; i < NORM_ROWS * groups; i += nt)
+        if (i % NORM_ROWS < rows) p.s[i / NORM_ROWS * p.lds + r0 + i % NORM_ROWS] = scales[i % NORM_ROWS][i / NORM_ROWS];
 }
 
 // Threads (a multiple of 64) that hold D columns in nv vectors of 8.
 static int norm_threads(int64_t D, int nv) { return (int)((D / 8 + nv - 1) / nv + 63) / 64 * 64; }
 
+// Two vectors a thread from 4096 columns on: 14 waves a row leave room for one
+// workgroup per CU, whose row sums nothing overlaps (8192 x 7168: 116 us
+// against 104 with 7 waves).  Rows per workgroup, a power of two: as many as
+// leave 14 waves on every CU (8192 x 7168 in 4, 8, 16 rows: 119, 107, 104
+// us; 8192 x 2048: 32, 29, 39 us).
 hipError_t launch_norm(const NormArgs& g, hipStream_t st) {
     if (g.M == 0 || g.D == 0) return hipSuccess;
-    const int64_t rows_per = g.M >= 4096 ? 8 : g.M >= 1024 ? 2 : 1;
+    const int nv = g.D <= 4096 ? 1 : g.D <= 8192 ? 2 : 4;
+    const dim3 nt(norm_threads(g.D, nv));
+    int64_t rows_per = 1;
+    while (rows_per < NORM_ROWS && g.M * (nt.x / 64) >= rows_per * 2 * 256 * 14) rows_per *= 2;
     const dim3 grid((unsigned)((g.M + rows_per - 1) / rows_per));
-    if (g.D <= 8192)
-        hipLaunchKernelGGL(norm_kernel<1>, grid, dim3(norm_threads(g.D, 1)), 0, st, g, rows_per);
-    else if (g.D <= 16384)
-        hipLaunchKernelGGL(norm_kernel<2>, grid, dim3(norm_threads(g.D, 2)), 0, st, g, rows_per);
+    if (nv == 1)
+        hipLaunchKernelGGL((norm_kernel<1, 512>), grid, nt, 0, st, g, rows_per);
+    else if (nv == 2)
+        hipLaunchKernelGGL((norm_kernel<2, 512>), grid, nt, 0, st, g, rows_per);
+    else if (nt.x <= 512)
+        hipLaunchKernelGGL((norm_kernel<4, 512>), grid, nt, 0, st, g, rows_per);
     else
-        hipLaunchKernelGGL(norm_kernel<4>, grid, dim3(norm_threads(g.D, 4)), 0, st, g, rows_per);
+        hipLaunchKernelGGL((norm_kernel<4, 1024>), grid, nt, 0, st, g, rows_per);
     return hipGetLastError();
 }
 
@@ -181,6 +227,10 @@ hipError_t launch_norm(const NormArgs& g, hipStream_t st) {
 //   sum z yhat = sum k (dx' + r_x v) - c r_x sum k xhat,  k = gate w_post yhat:
 // the three row sums come from one reduction.
 //
+// With A = sum over a gate row's rows of t yhat, column by column, dgate =
+// w_post A and dw_post = sum over gate rows of gate A, so the row loop holds
+// one sum for both.
+//
 // The column sums are held in fp32 registers over a workgroup's consecutive
 // rows, written as partials, and added in a fixed order by a second kernel.
 // A gate row whose rows all lie in one workgroup is written at once; one
@@ -192,6 +242,11 @@ __device__ __forceinline__ float* part_gate(const NormBwdArgs& p, int64_t b, int
     return p.ws + (b * 4 + 2 + slot) * p.D;
 }
 
+__device__ __forceinline__ void storef8(float* p, const float (&v)[8]) {
+    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 template <int NV>
 __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int64_t rows_per) {
     __shared__ float red[2][16][3];
@@ -199,51 +254,82 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int64_t r
     const int t = threadIdx.x, nt = blockDim.x;
     const int64_t r0 = blockIdx.x * rows_per, r1 = r0 + rows_per < p.M ? r0 + rows_per : p.M;
     const float inv_d = 1.0f / (float)p.D;
+    const bool scaled = p.gate || p.w_post;
     int64_t col[NV];
     bool on[NV];
-    float wpre[NV][8], wpost[NV][8], gate[NV][8];
-    float apre[NV][8], apost[NV][8], agate[NV][8];
+    float wpre[NV][8], gw[NV][8];  // w_pre; gate * w_post, or the one there is
+    float apre[NV][8], apost[NV][8], asum[NV][8];
+    uint4 nt_[NV], nh[NV], nx[NV], ny[NV];  // the next row's dx', dh, x', y
+    auto load = [&](int64_t r) {
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            nt_[j] = raw8(p.dxo + r * p.lddxo + col[j], on[j] && p.dxo);
+            if (p.dh) {
+                nh[j] = raw8(p.dh + r * p.lddh + col[j], on[j]);
+                nx[j] = raw8(p.xo + r * p.ldxo + col[j], on[j]);
+            }
+            if (p.y) ny[j] = raw8(p.y + r * p.ldy + col[j], on[j]);
+        }
+    };
 #pragma unroll
     for (int j = 0; j < NV; j++) {
         col[j] = 8 * (int64_t)(t + j * nt);
         on[j] = col[j] < p.D;
         if (p.dh) loadf8(p.w_pre + col[j], on[j], wpre[j]);
-        if (p.w_post) loadf8(p.w_post + col[j], on[j], wpost[j]);
+        if (p.w_post && !p.gate) loadf8(p.w_post + col[j], on[j], gw[j]);
 #pragma unroll
-        for (int k = 0; k < 8; k++) apre[j][k] = apost[j][k] = agate[j][k] = 0.f;
+        for (int k = 0; k < 8; k++) apre[j][k] = apost[j][k] = asum[j][k] = 0.f;
     }
-    int64_t have = -1;
-    auto flush = [&](int64_t last_row) {  // the gate row `have`, whose rows here end at last_row
-        const int64_t first = have * p.gate_rows;
+    if (r0 < r1) load(r0);
+    int64_t cur = p.gate ? r0 / p.gate_rows : 0;                // the gate row of `asum`
+    int64_t next_gate = p.gate ? cur * p.gate_rows : p.M;       // where the next one is taken up
+    auto flush = [&](int64_t last_row) {  // gate row `cur`, whose rows here end at last_row
+        const int64_t first = cur * p.gate_rows;
         const int64_t end = first + p.gate_rows < p.M ? first + p.gate_rows : p.M;
         const bool whole = first >= r0 && end == last_row;
-        float* to = whole ? p.dgate + have * p.D : part_gate(p, blockIdx.x, first <= r0 ? 0 : 1);
+        float* to = whole ? p.dgate + cur * p.D : part_gate(p, blockIdx.x, first <= r0 ? 0 : 1);
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            if (on[j]) {
-                *(float4*)(to + col[j]) = make_float4(agate[j][0], agate[j][1], agate[j][2], agate[j][3]);
-                *(float4*)(to + col[j] + 4) = make_float4(agate[j][4], agate[j][5], agate[j][6], agate[j][7]);
-            }
+            float g[8], w[8];
+            loadf8(p.gate + cur * p.D + col[j], on[j], g);
+            if (p.w_post) loadf8(p.w_post + col[j], on[j], w);
 #pragma unroll
-            for (int k = 0; k < 8; k++) agate[j][k] = 0.f;
+            for (int k = 0; k < 8; k++) {
+                apost[j][k] += g[k] * asum[j][k];
+                w[k] = p.w_post ? w[k] * asum[j][k] : asum[j][k];
+                asum[j][k] = 0.f;
+            }
+            if (on[j]) storef8(to + col[j], w);
         }
     };
     for (int64_t r = r0; r < r1; r++) {
         float dxo[NV][8], dh[NV][8], xo[NV][8], y[NV][8];
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            load8(p.dxo + r * p.lddxo + col[j], on[j] && p.dxo, dxo[j]);
+            widen8(nt_[j], dxo[j]);
             if (p.dh) {
-                load8(p.dh + r * p.lddh + col[j], on[j], dh[j]);
-                load8(p.xo + r * p.ldxo + col[j], on[j], xo[j]);
+                widen8(nh[j], dh[j]);
+                widen8(nx[j], xo[j]);
             }
-            if (p.y) load8(p.y + r * p.ldy + col[j], on[j], y[j]);
+            if (p.y) widen8(ny[j], y[j]);
         }
-        if (p.gate && r / p.gate_rows != have) {
-            if (have >= 0) flush(r);
-            have = r / p.gate_rows;
+        if (r + 1 < r1) load(r + 1);
+        if (r >= next_gate) {
+            if (r > r0) {
+                flush(r);
+                cur++;
+            }
 #pragma unroll
-            for (int j = 0; j < NV; j++) loadf8(p.gate + have * p.D + col[j], on[j], gate[j]);
+            for (int j = 0; j < NV; j++) {
+                loadf8(p.gate + cur * p.D + col[j], on[j], gw[j]);
+                if (p.w_post) {
+                    float w[8];
+                    loadf8(p.w_post + col[j], on[j], w);
+#pragma unroll
+                    for (int k = 0; k < 8; k++) gw[j][k] *= w[k];
+                }
+            }
+            next_gate += p.gate_rows;
         }
         const float rx = p.dh ? p.rstd_x[r] : 0.f;
         const float ry = p.w_post ? p.rstd_y[r] : 1.f;
@@ -262,9 +348,9 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int64_t r
                     dxo[j][k] += rx * v;
                     xo[j][k] = xhat;
                 }
+                if (p.y) y[j][k] *= ry;
                 if (p.w_post) {
-                    float q = wpost[j][k] * (y[j][k] * ry);
-                    if (p.gate) q *= gate[j][k];
+                    const float q = gw[j][k] * y[j][k];
                     s[1] += q * dxo[j][k];
                     s[2] += q * xhat;
                 }
@@ -284,35 +370,20 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int64_t r
             if (!p.y) continue;
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                float n = y[j][k], dn = dxo[j][k];
-                const float yhat = n * ry;
-                if (p.w_post) n = yhat * wpost[j][k];
-                if (p.gate) {
-                    agate[j][k] += dn * n;
-                    dn *= gate[j][k];
-                }
-                if (p.w_post) {
-                    apost[j][k] += dn * yhat;
-                    dn = ry * (dn * wpost[j][k] - yhat * m);
-                }
-                o[k] = dn;
+                if (scaled) asum[j][k] += dxo[j][k] * y[j][k];
+                o[k] = scaled ? dxo[j][k] * gw[j][k] : dxo[j][k];
+                if (p.w_post) o[k] = ry * (o[k] - y[j][k] * m);
             }
             if (on[j]) store8(p.dy + r * p.lddy + col[j], o);
         }
     }
-    if (p.gate && have >= 0) flush(r1);
+    if (p.gate && r0 < r1) flush(r1);
 #pragma unroll
     for (int j = 0; j < NV; j++) {
         if (!on[j]) continue;
         float* w = part_pre(p, blockIdx.x) + col[j];
-        if (p.dh) {
-            *(float4*)w = make_float4(apre[j][0], apre[j][1], apre[j][2], apre[j][3]);
-            *(float4*)(w + 4) = make_float4(apre[j][4], apre[j][5], apre[j][6], apre[j][7]);
-        }
-        if (p.w_post) {
-            *(float4*)(w + p.D) = make_float4(apost[j][0], apost[j][1], apost[j][2], apost[j][3]);
-            *(float4*)(w + p.D + 4) = make_float4(apost[j][4], apost[j][5], apost[j][6], apost[j][7]);
-        }
+        if (p.dh) storef8(w, apre[j]);
+        if (p.w_post) storef8(w + p.D, p.gate ? apost[j] : asum[j]);
     }
 }
 
@@ -364,26 +435,38 @@ __global__ __launch_bounds__(1024) void norm_bwd_reduce_kernel(NormBwdArgs p, in
     }
 }
 
-int norm_bwd_parts(int64_t M) {
-    const int64_t per = (M + 511) / 512;
-    return M == 0 ? 0 : (int)((M + per - 1) / per);
+// One vector a thread up to 8192 columns, at 128 registers (8192 x 7168: 187
+// us; two vectors at 247 registers 222 us, with half the waves to a CU).
+static int norm_bwd_nv(int64_t D) { return D <= 8192 ? 1 : D <= 16384 ? 2 : 4; }
+
+// Workgroups: as many as run at once (16 waves a CU), so that the partials
+// stay few: each is up to 16 B per column.
+int norm_bwd_parts(int64_t M, int64_t D) {
+    if (M == 0 || D == 0) return 0;
+    const int nv = norm_bwd_nv(D);
+    int64_t per_cu = 16 / (norm_threads(D, nv) / 64 * nv);
+    if (per_cu > 4) per_cu = 4;
+    if (per_cu < 1) per_cu = 1;
+    const int64_t per = (M + 256 * per_cu - 1) / (256 * per_cu);
+    return (int)((M + per - 1) / per);
 }
 
 size_t norm_bwd_workspace(int64_t M, int64_t D) {
-    return (size_t)norm_bwd_parts(M) * 4 * (size_t)D * sizeof(float);
+    return (size_t)norm_bwd_parts(M, D) * 4 * (size_t)D * sizeof(float);
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& g, hipStream_t st) {
     if (g.D == 0) return hipSuccess;
     const int64_t rows_per = (g.M + g.parts - 1) / (g.parts > 0 ? g.parts : 1);
     if (g.M > 0) {
-        const dim3 grid((unsigned)g.parts);
-        if (g.D <= 8192)
-            hipLaunchKernelGGL(norm_bwd_kernel<1>, grid, dim3(norm_threads(g.D, 1)), 0, st, g, rows_per);
-        else if (g.D <= 16384)
-            hipLaunchKernelGGL(norm_bwd_kernel<2>, grid, dim3(norm_threads(g.D, 2)), 0, st, g, rows_per);
+        const int nv = norm_bwd_nv(g.D);
+        const dim3 grid((unsigned)g.parts), nt(norm_threads(g.D, nv));
+        if (nv == 1)
+            hipLaunchKernelGGL(norm_bwd_kernel<1>, grid, nt, 0, st, g, rows_per);
+        else if (nv == 2)
+            hipLaunchKernelGGL(norm_bwd_kernel<2>, grid, nt, 0, st, g, rows_per);
         else
-            hipLaunchKernelGGL(norm_bwd_kernel<4>, grid, dim3(norm_threads(g.D, 4)), 0, st, g, rows_per);
+            hipLaunchKernelGGL(norm_bwd_kernel<4>, grid, nt, 0, st, g, rows_per);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
