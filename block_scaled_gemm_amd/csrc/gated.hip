@@ -53,6 +53,80 @@ __device__ __forceinline__ uint32_t pk_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2){lo, hi}, bf2));
 }
 
+// ==== experts' row tiles =====================================================================
+//
+// Every expert's rows are cut into tiles of TILE rows from its first one on.
+// Tile `u`, counted over all experts: its expert, first row and how many rows
+// it holds (0: there is no such tile).  Called by THREADS threads; every thread
+// gets the answer.
+
+struct RowTile {
+    int64_t expert, row0;
+    int rows;
+    bool only;  // its expert's only tile
+};
+
+template <int TILE>
+__device__ __forceinline__ int64_t count_tiles(const int32_t* __restrict__ offsets, int G) {
+    __shared__ int64_t wsum[THREADS / 64];
+    const int t = threadIdx.x;
+    int64_t n = 0;
+    for (int e = t; e < G; e += THREADS) n += ((int64_t)offsets[e + 1] - offsets[e] + TILE - 1) / TILE;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) n += __shfl_xor(n, d);
+    if ((t & 63) == 0) wsum[t >> 6] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; w++) n += wsum[w];
+    return n;
+}
+
+template <int TILE>
+__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, int G, int64_t u) {
+    __shared__ int64_t wsum[THREADS / 64];
+    __shared__ RowTile found;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    if (t == 0) found.rows = 0;
+    int64_t base = 0;
+    for (int e0 = 0; e0 < G; e0 += THREADS) {
+        const int e = e0 + t;
+        int64_t lo = 0, n = 0;
+        if (e < G) {
+            lo = offsets[e];
+            n = (int64_t)offsets[e + 1] - lo;
+        }
+        const int64_t mine = (n + TILE - 1) / TILE;
+        int64_t incl = mine;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_up(incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 63) wsum[wave] = incl;
+        __syncthreads();
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 64; w++) {
+            if (w < wave) incl += wsum[w];
+            total += wsum[w];
+        }
+        incl += base;
+        if (incl > u && incl - mine <= u) {
+            const int64_t at = (u - (incl - mine)) * TILE;
+            found.expert = e;
+            found.row0 = lo + at;
+            found.rows = (int)(n - at < TILE ? n - at : TILE);
+            found.only = n <= TILE;
+        }
+        base += total;
+        __syncthreads();
+        if (base > u) break;  // workgroup-uniform
+    }
+    __syncthreads();
+    return found;
+}
+
 // ==== forward: tiles =======================================================================
 //
 // All shapes hold 256 B rows: 128 gate and 128 up rows of the same columns,
@@ -93,6 +167,26 @@ struct Shape<22> {
     }
 };
 
+//  Shape 23: 32 rows, waves of 32 x 32, three stages: the f16 path with at most
+//    32 rows.  A wave's 32 LDS rows are 8 gate, 8 up, 8 gate and 8 up rows, so
+//    that one 32 x 32 MFMA leaves G and U of a column in the same lane.
+template <>
+struct Shape<23> {
+    static constexpr int BM = 32, BN = 256;
+    static constexpr int WM = 32, WN = 32;
+    static constexpr int STAGES = 3;
+    __device__ static void wave_grid(int wave, int& wm, int& wn) {
+        wm = 0;
+        wn = wave;
+    }
+};
+
+// The two block scalars of a stage: one direct load fills 64 row scales, also
+// where the tile has fewer rows, and the scalars lie behind them.
+template <int SH>
+constexpr int kScalars = Lds<SH>::SA + (Shape<SH>::BM > 64 ? Shape<SH>::BM : 64) * 4;
+static_assert(kScalars<23> + 256 <= Lds<23>::STAGE && kScalars<21> == Lds<21>::SB, "inside the stage");
+
 struct GTile {
     int64_t m0, m_end;  // rows [m0, min(m0+BM, m_end)) are real
     int64_t n0;         // 128 output columns
@@ -105,6 +199,7 @@ struct GTile {
     int64_t ldb;
     const float* sb;   // gate block row n0/128; the up one is sb_up floats on
     uint32_t sb_up;
+    bool stream;
 };
 
 // As Stager: per-lane source offsets fixed per tile, wave-uniform bases that
@@ -112,13 +207,14 @@ struct GTile {
 // its first ones, so one per-lane offset serves them (eight registers fewer,
 // which the 64 x 128 wave tile does not have).  On the shorter tiles a loader
 // issues only the A instructions whose 8-row block holds a row of the tile.
-// NT: weights with the non-temporal hint (experts: each weight tile streams
-// through once).
-template <int SH, bool NT>
+// T.stream: weights with the non-temporal hint, where no other row tile reads
+// them (an expert of at most one tile).
+template <int SH>
 struct GStager {
-    static constexpr int BM = Shape<SH>::BM, BN = Shape<SH>::BN, WN = Shape<SH>::WN;
+    static constexpr int BM = Shape<SH>::BM, BN = Shape<SH>::BN;
+    static constexpr int WN = SH == 23 ? 16 : Shape<SH>::WN;  // gate and up rows alternate in halves of WN
     static constexpr int NA = BM / 8 / LOADERS, NB = BN / 8 / LOADERS;
-    static constexpr int SA_INS = BM / 64;
+    static constexpr int SA_INS = (BM + 63) / 64;
     static constexpr bool SKIP = BM < 256;
     static_assert(BN == 256 && SA_INS <= LOADERS, "one gate and one up block per tile");
     uint32_t va[NA], vb, vsa, vsb;
@@ -162,13 +258,13 @@ struct GStager {
         for (int ins = 0; ins < NB; ins++) {
             const int row = (ins * LOADERS + wave) * 8;
             const uint8_t* b = (is_up(row) ? T.bu : T.bg) + col_of(row) * T.ldb + g * 128;
-            if (NT)
+            if (T.stream)
                 dma16s_nt(vb, b, base + Lds<SH>::B + row * 128);
             else
                 dma16s(vb, b, base + Lds<SH>::B + row * 128);
         }
         if (wave < SA_INS) dma4s(vsa, T.sa + g * T.ldsa + T.m0, base + Lds<SH>::SA + wave * 256);
-        if (wave == 0) dma4s(vsb, T.sb + g, base + Lds<SH>::SB);
+        if (wave == 0) dma4s(vsb, T.sb + g, base + kScalars<SH>);
     }
 };
 
@@ -182,7 +278,7 @@ __device__ __forceinline__ void gated_group8(const uint8_t* stage, int wm, int w
     const uint8_t* la = stage + Lds<SH>::A;
     const uint8_t* lb = stage + Lds<SH>::B;
     const float* lsa = (const float*)(stage + Lds<SH>::SA);
-    const float* lsb = (const float*)(stage + Lds<SH>::SB);
+    const float* lsb = (const float*)(stage + kScalars<SH>);
     const int mbase = wm * Shape<SH>::WM, nbase = wn * Shape<SH>::WN;
     const int c0 = 2 * (lane >> 4);
     // a wave whose rows are all past the end multiplies them all the same:
@@ -266,7 +362,7 @@ __device__ __forceinline__ void gated_group16(const uint8_t* stage, int wm, int 
     const uint8_t* la = stage + Lds<SH>::A;
     const uint8_t* lb = stage + Lds<SH>::B;
     const float* lsa = (const float*)(stage + Lds<SH>::SA);
-    const float* lsb = (const float*)(stage + Lds<SH>::SB);
+    const float* lsb = (const float*)(stage + kScalars<SH>);
     const int mbase = wm * 64, nbase = wn * 64;
     const int r = lane & 31, h = lane >> 5;
 
@@ -319,6 +415,38 @@ __device__ __forceinline__ void gated_group16(const uint8_t* stage, int wm, int 
     for (int i = 0; i < 2; i++)
 #pragma unroll
         for (int j = 0; j < 2; j++) cp[i][j] = cn[i][j];
+}
+
+// The same on the 32-row tile: one 32 x 32 sub-tile, registers 8q..8q+3 the
+// gate's columns 8q' and 8q+4..8q+7 the up's (q' the 16-row block).
+__device__ __forceinline__ void gated_group16_32(const uint8_t* stage, int wn, int lane, v16f& acc, v16f& p,
+                                                 float (&cp)[2]) {
+    constexpr int SH = 23;
+    const uint8_t* la = stage + Lds<SH>::A;
+    const uint8_t* lb = stage + Lds<SH>::B;
+    const float* lsb = (const float*)(stage + kScalars<SH>);
+    const int r = lane & 31, h = lane >> 5;
+    const float sam = ((const float*)(stage + Lds<SH>::SA))[r];
+    const float c0 = sam * lsb[0], c1 = sam * lsb[1];
+    uint4 ra[4], rb[4];
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        ra[q] = lds16(la, r, 2 * q + h);
+        rb[q] = lds16(lb, 32 * wn + r, 2 * q + h);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; k++) acc[k] += p[k] * cp[(k >> 2) & 1];
+    const v16f zero = {};
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+        v8h a0, a1, b0, b1;
+        widen16(ra[q], a0, a1);
+        widen16(rb[q], b0, b1);
+        p = __builtin_amdgcn_mfma_f32_32x32x16_f16(b0, a0, q == 0 ? zero : p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_32x32x16_f16(b1, a1, p, 0, 0, 0);
+    }
+    cp[0] = c0;
+    cp[1] = c1;
 }
 
 // ==== forward: epilogue ======================================================================
@@ -411,12 +539,13 @@ __device__ __forceinline__ void gated_epilogue(const GatedArgs& p, const GTile& 
 
 // ==== forward: one tile ======================================================================
 
-template <int ACC, int SH, bool NT>
+template <int ACC, int SH>
 __device__ __forceinline__ void gated_tile(const GatedArgs& p, const GTile& T, int64_t g0, int64_t g1, int64_t split,
                                            uint8_t* smem) {
     constexpr int S = Shape<SH>::STAGES, BM = Shape<SH>::BM, WM = Shape<SH>::WM, WN = Shape<SH>::WN;
     static_assert(BM * GLD * 4 <= Lds<SH>::BYTES, "the image fits in the stages");
-    static_assert(ACC != 0 || SH == 21, "the f16 path runs on 64 x 64 wave tiles");
+    static_assert(ACC != 0 || SH == 21 || SH == 23, "the f16 path's wave tiles");
+    constexpr bool SMALL16 = ACC == 0 && SH == 23;
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     int wm, wn;
@@ -424,11 +553,15 @@ __device__ __forceinline__ void gated_tile(const GatedArgs& p, const GTile& T, i
     const int m_valid = (int)(T.m_end - T.m0 < BM ? T.m_end - T.m0 : BM);
 
     constexpr int MI = Sub<SH>::MI, NJ = Sub<SH>::NJ;
-    typedef typename std::conditional<ACC == 0, v16f[2][2], v4f[MI][NJ]>::type AccT;
+    typedef typename std::conditional<SMALL16, v16f,
+                                      typename std::conditional<ACC == 0, v16f[2][2], v4f[MI][NJ]>::type>::type AccT;
     AccT acc;
     v16f pp[2][2];
     float cp[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-    if constexpr (ACC == 0) {
+    if constexpr (SMALL16) {
+#pragma unroll
+        for (int r = 0; r < 16; r++) acc[r] = pp[0][0][r] = 0.f;
+    } else if constexpr (ACC == 0) {
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll
@@ -442,24 +575,26 @@ __device__ __forceinline__ void gated_tile(const GatedArgs& p, const GTile& T, i
             for (int j = 0; j < NJ; j++) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
     }
 
-    GStager<SH, NT> stg;
+    GStager<SH> stg;
     stg.init(T, wave, lane);
 #pragma unroll
     for (int s = 0; s < S - 1; s++)
         if (g0 + s < g1) stg.issue(T, g0 + s, smem, s * Lds<SH>::STAGE, wave);
     // a loader's tile loads per group; its scale loads come on top, so
     // waiting for `per` outstanding is conservative
-    const int per = stg.na_valid + GStager<SH, NT>::NB;
+    const int per = stg.na_valid + GStager<SH>::NB;
     static_assert(S == 2 || S == 3, "wait counts cover this pipeline");
     auto step = [&](auto ss, int64_t g) {
         constexpr int SS = decltype(ss)::value;
         if (S == 3 && g + 1 < g1 && wave < LOADERS)
-            wait_n_and_barrier<GStager<SH, NT>::NA + GStager<SH, NT>::NB>(per);
+            wait_n_and_barrier<GStager<SH>::NA + GStager<SH>::NB>(per);
         else
             wait_and_barrier<0>(wave);
         if (g + S - 1 < g1) stg.issue(T, g + S - 1, smem, ((SS + S - 1) % S) * Lds<SH>::STAGE, wave);
         const uint8_t* stage = smem + SS * Lds<SH>::STAGE;
-        if constexpr (ACC == 0) {
+        if constexpr (SMALL16) {
+            gated_group16_32(stage, wn, lane, acc, pp[0][0], cp[0]);
+        } else if constexpr (ACC == 0) {
             if (wm * 64 < m_valid) gated_group16(stage, wm, wn, lane, acc, pp, cp);
         } else {
             gated_group8<ACC, SH>(stage, wm, wn, lane, acc);
@@ -471,7 +606,10 @@ __device__ __forceinline__ void gated_tile(const GatedArgs& p, const GTile& T, i
         if constexpr (S == 3)
             if (g + 2 < g1) step(std::integral_constant<int, 2>(), g + 2);
     }
-    if constexpr (ACC == 0) {
+    if constexpr (SMALL16) {
+#pragma unroll
+        for (int k = 0; k < 16; k++) acc[k] += pp[0][0][k] * cp[0][(k >> 2) & 1];
+    } else if constexpr (ACC == 0) {
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll
@@ -480,7 +618,19 @@ __device__ __forceinline__ void gated_tile(const GatedArgs& p, const GTile& T, i
     wait_and_barrier<0>(wave);  // the stages hold the images next
 
     gated_epilogue(p, T, BM, split, smem, [&](float* ep, int which) {
-        if constexpr (ACC == 0) {
+        if constexpr (SMALL16) {
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float g = acc[8 * q + e], u = acc[8 * q + 4 + e];
+                    v[e] = which == 0 ? g : which == 1 ? u : gated(p.act, g, u);
+                }
+                *(float4*)&ep[(lane & 31) * GLD + wn * 16 + 8 * q + 4 * (lane >> 5)] =
+                    make_float4(v[0], v[1], v[2], v[3]);
+            }
+        } else if constexpr (ACC == 0) {
 #pragma unroll
             for (int i = 0; i < 2; i++)
 #pragma unroll
@@ -524,6 +674,7 @@ __device__ __forceinline__ GTile gated_operands(const GatedArgs& p, int64_t e, i
     T.ldb = p.ldb;
     T.sb = p.sb + e * p.sb_estride + (n0 >> 7) * p.ldsb;
     T.sb_up = (uint32_t)((p.N >> 7) * p.ldsb);
+    T.stream = false;
     return T;
 }
 
@@ -542,37 +693,42 @@ __global__ __launch_bounds__(THREADS) void gated_kernel(GatedArgs p, int64_t til
     const int64_t per = (groups + p.splits - 1) / p.splits;
     const int64_t g0 = split * per < groups ? split * per : groups;
     const int64_t g1 = g0 + per < groups ? g0 + per : groups;
-    gated_tile<ACC, SH, false>(p, T, g0, g1, split, smem);
+    gated_tile<ACC, SH>(p, T, g0, g1, split, smem);
 }
 
-// Experts: workgroup (expert, 128 columns) walks the expert's rows, so each
-// weight tile leaves HBM once.
+// Experts: a workgroup takes one row tile of an expert and 128 columns.  How
+// many row tiles there are only the offsets say, so the grid holds the most
+// there can be (one more per expert than the rows fill) and the workgroups
+// past the last tile leave.  A workgroup to each row tile, and not to each
+// expert's rows, evens out experts of uneven size (32 experts, 4096 rows: 322
+// us with a workgroup walking its expert's rows).
 template <int ACC>
 __global__ __launch_bounds__(THREADS) void gated_grouped_kernel(GatedArgs p, int64_t tiles_n) {
+    constexpr int TILE = Shape<ACC == 0 ? 21 : 20>::BM;
     constexpr int BYTES = ACC == 0 ? Lds<21>::BYTES : Lds<21>::BYTES > Lds<20>::BYTES ? Lds<21>::BYTES : Lds<20>::BYTES;
     static_assert(Lds<22>::BYTES <= BYTES, "every row-tile shape fits");
     __shared__ __attribute__((aligned(16))) uint8_t smem[BYTES];
-    const int64_t wid = xcd_remap(blockIdx.x, gridDim.x);
-    const int64_t e = wid / tiles_n;
-    const int64_t r0 = p.offsets[e], r1 = p.offsets[e + 1];
-    GTile T = gated_operands(p, e, (wid % tiles_n) * 128);
-    T.m_end = r1;
+    const int64_t total = count_tiles<TILE>(p.offsets, p.G) * tiles_n;
+    if ((int64_t)blockIdx.x >= total) return;  // workgroup-uniform
+    const int64_t wid = xcd_remap(blockIdx.x, total);
+    const RowTile f = find_tile<TILE>(p.offsets, p.G, wid / tiles_n);
+    GTile T = gated_operands(p, f.expert, (wid % tiles_n) * 128);
+    T.m0 = f.row0;
+    T.m_end = f.row0 + f.rows;
+    T.stream = f.only;
     const int64_t groups = p.K / 128;
     if constexpr (ACC == 0) {
-        for (int64_t m0 = r0; m0 < r1; m0 += Shape<21>::BM) {
-            T.m0 = m0;
-            gated_tile<0, 21, true>(p, T, 0, groups, 0, smem);
-        }
+        if (f.rows <= Shape<23>::BM)
+            gated_tile<0, 23>(p, T, 0, groups, 0, smem);
+        else
+            gated_tile<0, 21>(p, T, 0, groups, 0, smem);
     } else {
-        for (int64_t m0 = r0; m0 < r1; m0 += Shape<20>::BM) {
-            T.m0 = m0;
-            if (r1 - m0 <= Shape<22>::BM)
-                gated_tile<ACC, 22, true>(p, T, 0, groups, 0, smem);
-            else if (r1 - m0 <= Shape<21>::BM)
-                gated_tile<ACC, 21, true>(p, T, 0, groups, 0, smem);
-            else
-                gated_tile<ACC, 20, true>(p, T, 0, groups, 0, smem);
-        }
+        if (f.rows <= Shape<22>::BM)
+            gated_tile<ACC, 22>(p, T, 0, groups, 0, smem);
+        else if (f.rows <= Shape<21>::BM)
+            gated_tile<ACC, 21>(p, T, 0, groups, 0, smem);
+        else
+            gated_tile<ACC, 20>(p, T, 0, groups, 0, smem);
     }
 }
 
@@ -635,7 +791,10 @@ static void launch_gated_shape(const GatedArgs& g, hipStream_t st) {
 template <int ACC>
 static void launch_gated_acc(const GatedArgs& g, hipStream_t st) {
     if constexpr (ACC == 0) {
-        launch_gated_shape<0, 21>(g, st);
+        if (g.M <= Shape<23>::BM)
+            launch_gated_shape<0, 23>(g, st);
+        else
+            launch_gated_shape<0, 21>(g, st);
     } else {
         if (g.M <= Shape<22>::BM)
             launch_gated_shape<ACC, 22>(g, st);
@@ -664,7 +823,12 @@ hipError_t launch_gated(const GatedArgs& g, hipStream_t st) {
 hipError_t launch_grouped_gated(const GatedArgs& g, hipStream_t st) {
     if (g.G == 0 || g.N == 0) return hipSuccess;
     const int64_t tiles_n = g.N / 128;
-    const dim3 grid((unsigned)(tiles_n * g.G));
+    const int64_t tile = g.accum == 0 ? Shape<21>::BM : Shape<20>::BM;
+    // the rows fill at most this many tiles, no expert more than its own, and a
+    // last tile each
+    int64_t most = (g.M + tile - 1) / tile + g.G;
+    if (most > g.M) most = g.M;
+    const dim3 grid((unsigned)(tiles_n * most));
     if (g.accum == 0)
         hipLaunchKernelGGL(gated_grouped_kernel<0>, grid, dim3(THREADS), 0, st, g, tiles_n);
     else if (g.accum == 1)
@@ -690,7 +854,7 @@ hipError_t launch_grouped_gated(const GatedArgs& g, hipStream_t st) {
 // registers a thread and 78 KB, two workgroups share a CU and one's loads
 // overlap the other's arithmetic.
 
-constexpr int BT = 512;
+constexpr int BT = THREADS;
 
 // Max over the four 16-lane DPP rows of the wave, lane by lane, of values >= 0
 // (gfx950's row and half-wave swaps: both results hold one of the two sides).
@@ -726,54 +890,6 @@ __device__ __forceinline__ void st_stream8(uint8_t* p, uint32_t lo, uint32_t hi)
     __builtin_nontemporal_store((u32x2_s){lo, hi}, (u32x2_s*)p);
 }
 
-// The rows of padded group `pg`: first row and how many of its 128 are real
-// (0: no such group).  Every expert starts a group of its own.  `found` is
-// workgroup-shared; every thread gets the answer.
-__device__ __forceinline__ void find_group(const int32_t* __restrict__ offsets, int G, int64_t pg, int64_t& row0,
-                                           int& rows) {
-    __shared__ int64_t wsum[BT / 64];
-    __shared__ int64_t found_row;
-    __shared__ int found_rows;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    if (t == 0) found_rows = 0;
-    int64_t base = 0;
-    for (int e0 = 0; e0 < G; e0 += BT) {
-        const int e = e0 + t;
-        int64_t lo = 0, n = 0;
-        if (e < G) {
-            lo = offsets[e];
-            n = (int64_t)offsets[e + 1] - lo;
-        }
-        const int64_t mine = (n + 127) / 128;
-        int64_t incl = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t o = __shfl_up(incl, d);
-            if (lane >= d) incl += o;
-        }
-        if (lane == 63) wsum[wave] = incl;
-        __syncthreads();
-        int64_t total = 0;
-#pragma unroll
-        for (int w = 0; w < BT / 64; w++) {
-            if (w < wave) incl += wsum[w];
-            total += wsum[w];
-        }
-        incl += base;
-        if (incl > pg && incl - mine <= pg) {
-            const int64_t at = (pg - (incl - mine)) * 128;
-            found_row = lo + at;
-            found_rows = (int)(n - at < 128 ? n - at : 128);
-        }
-        base += total;
-        __syncthreads();
-        if (base > pg) break;  // workgroup-uniform
-    }
-    __syncthreads();
-    row0 = found_row;
-    rows = found_rows;
-}
-
 template <bool POW2, int ACT>
 __global__ __launch_bounds__(BT) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_kernel(
     GatedBwdArgs p, int64_t col_tiles) {
@@ -788,7 +904,9 @@ __global__ __launch_bounds__(BT) __attribute__((amdgpu_waves_per_eu(4, 4))) void
     int64_t row0 = pg * 128;
     int rows = (int)(p.M - row0 < 128 ? p.M - row0 : 128);
     if (p.offsets) {
-        find_group(p.offsets, p.G, pg, row0, rows);
+        const RowTile f = find_tile<128>(p.offsets, p.G, pg);
+        row0 = f.row0;
+        rows = f.rows;
         if (rows <= 0) return;  // workgroup-uniform: past the last group
     }
 

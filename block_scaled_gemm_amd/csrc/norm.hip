@@ -420,11 +420,15 @@ __global__ __launch_bounds__(1024) void norm_bwd_reduce_kernel(NormBwdArgs p, in
         to = p.dgate + row * p.D;
     }
     if (!to) return;
+    // the gate row's partial is in its first workgroup's second slot unless it
+    // starts with the workgroup, and in the others' first
+    const float* from = p.ws + kind * p.D + c;
+    const int64_t late = kind == 2 && row * p.gate_rows > b0 * rows_per ? p.D : 0;
     float v = 0.f;
-    if (c < p.D)
-        for (int64_t b = b0 + run; b < b1; b += 16)
-            v += kind == 2 ? part_gate(p, b, row * p.gate_rows <= b * rows_per ? 0 : 1)[c]
-                           : (part_pre(p, b) + kind * p.D)[c];
+    if (c < p.D) {
+#pragma unroll 8
+        for (int64_t b = b0 + run; b < b1; b += 16) v += from[b * 4 * p.D + (b == b0 ? late : 0)];
+    }
     lds[run][lane] = v;
     __syncthreads();
     if (run == 0 && c < p.D) {
