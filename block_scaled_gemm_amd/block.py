@@ -5,12 +5,13 @@ As the rest of the binding, argument marshalling only; the contracts stand in
 include/fp8bs.h.  Tensors have to live on the current device, and every call
 is enqueued on its current stream.
 """
+import array
 import collections
 import ctypes
 
 import torch
 
-from . import (ACCUM_FP32, ACCUM_MFMA8_POW2, OUT_BF16, OUT_F32, SCALE_FP32, _check, _check_pow2_mode, _ptr, _stream,
+from . import (ACCUM_FP32, ACCUM_MFMA8_POW2, OUT_BF16, OUT_F32, SCALE_FP32, _check, _check_pow2_mode, _ptr,
                grouped_col_bound, lib)
 
 ACT_SILU, ACT_GELU = 0, 1
@@ -25,7 +26,7 @@ def declare(L):
     kept = [vp, i64, i32]
     quant = [i32, vp, i64, vp, i64]
     for name, res, args in [
-            ("fp8_gated_workspace_bytes", sz, [i64] * 3),
+            ("fp8_gated_workspace_bytes", sz, [i64] * 3 + [i32]),
             ("fp8_gated_gemm", i32, [i64] * 3 + gated + [vp, i64, i32] + kept + [vp, sz, vp]),
             ("fp8_gated_gemm_quant", i32, [i64] * 3 + gated + quant + kept + [vp, sz, vp]),
             ("fp8_grouped_gated_gemm", i32,
@@ -47,88 +48,132 @@ def declare(L):
         f.restype, f.argtypes = res, args
 
 
-def _need(t, name, dtype, *shape):
-    """Checks a tensor the kernels will address: on the current device, of the
-    type, of the shape (an entry None is free; an int is a lower bound in the
-    first dimension and exact in the last), its last dimension contiguous."""
+def _arg(t, name, dtype, dev, shape, least=False):
+    """(address, leading dimension) of a tensor the kernels will address:
+    on the current device, of the type and shape (None: any extent), its last
+    dimension contiguous.  least: `shape` is a lower bound in the first
+    dimension of a matrix."""
+    # the usual case first: these checks are most of a small call's time
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape and \
+            t.is_contiguous():
+        return t.data_ptr(), shape[-1]
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is {torch.cuda.current_device()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is {dev}")
     size = t.shape
-    if len(size) != len(shape):
-        raise ValueError(f"{name} must have {len(shape)} dimensions, got {tuple(size)}")
-    last = len(shape) - 1
-    for i, want in enumerate(shape):
-        if want is not None and (size[i] != want if i == last else size[i] < want):
-            raise ValueError(f"{name} has shape {tuple(size)}, needs {shape}")
-    if size[last] > 1 and t.stride(last) != 1:
+    if len(size) != len(shape) or any(
+            want is not None and (have < want if least and i == 0 else have != want)
+            for i, (have, want) in enumerate(zip(size, shape))):
+        raise ValueError(f"{name} has shape {tuple(size)}, needs {tuple(shape)}")
+    if size[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
+    if len(size) > 2 and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if len(size) == 1:
+        return t.data_ptr(), size[0]
+    # of a single row, any leading dimension that the library takes
+    return t.data_ptr(), t.stride(0) if size[0] > 1 else max(t.stride(0), size[1] + -size[1] % 16)
 
 
-def _ld(t):
-    """Leading dimension of a matrix; of one row, any that the library takes."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] + -t.shape[1] % 16)
+def _scales(t, name, dev, groups, rows):
+    """(address, leading dimension) of group-major scales [groups, >= rows]."""
+    if isinstance(t, torch.Tensor) and t.dim() == 2 and t.shape[1] > rows:
+        return _arg(t, name, F32, dev, (groups, None))
+    return _arg(t, name, F32, dev, (groups, rows))
 
 
 def _new(shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def gated_workspace_bytes(M, N, K):
-    return int(lib().fp8_gated_workspace_bytes(M, N, K))
+def _device(t, name):
+    """The current device, for a call whose sizes the tensor t gives."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    return torch.cuda.current_device()
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _out(t, name, dtype, dev, shape, like):
+    """(tensor, address, leading dimension) of an output, allocated where not given."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t, t.data_ptr(), shape[1]
+    return (t, *_arg(t, name, dtype, dev, shape, True))
+
+
+def _quant_out(q, s, M, N, dev, like):
+    """Codes [M, N] and scales [N/128, M]: (q, s, their addresses and leading dimensions)."""
+    q, qp, ldq = _out(q, "q", U8, dev, (M, N), like)
+    if s is None:
+        s = torch.empty((N // 128, M), dtype=F32, device=like.device)
+    sp, lds = _scales(s, "s", dev, N // 128, M)
+    return q, s, (qp, ldq, sp, lds)
+
+
+def _workspace(t, need, dev, like):
+    """(address, bytes) of device scratch, allocated where not given."""
+    if need == 0:
+        return None, 0
+    if t is None:
+        t = torch.empty(need, dtype=U8, device=like.device)
+    return _arg(t, "workspace", U8, dev, (None,))
+
+
+def _stream_of(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def gated_workspace_bytes(M, N, K, quant=False):
+    return int(lib().fp8_gated_workspace_bytes(M, N, K, quant))
 
 
 # ---- gated products ------------------------------------------------------------------
 
-def _gated_operands(a, sa, b, sb, accum, rows=None, offsets=None):
-    """Checks the operands; returns (M, N, K, G or None)."""
-    _need(a, "a", U8, None, None)
-    K = a.shape[1]
-    M = a.shape[0] if rows is None else int(rows)
-    if not 0 <= M <= a.shape[0]:
-        raise ValueError(f"rows_bound {M} outside the {a.shape[0]} rows of a")
-    _need(sa, "sa", F32, K // 128, None)
-    if sa.shape[1] < M:
-        raise ValueError(f"sa has {sa.shape[1]} rows' scales, needs {M}")
+def _gated_operands(a, sa, b, sb, accum, dev, rows=None, offsets=None):
+    """Checks the operands; returns (M, N, K, G or None, the operands'
+    addresses and leading dimensions)."""
+    R, K = _matrix(a, "a")
+    M = R if rows is None else int(rows)
+    if not 0 <= M <= R:
+        raise ValueError(f"rows_bound {M} outside the {R} rows of a")
+    ap, lda = _arg(a, "a", U8, dev, (R, K))
+    sap, ldsa = _scales(sa, "sa", dev, K // 128, M)
     if offsets is None:
-        _need(b, "b", U8, None, K)
-        G, R = None, b.shape[0]
-        _need(sb, "sb", F32, R // 128, K // 128)
+        if not isinstance(b, torch.Tensor):
+            raise TypeError("b must be a CUDA (HIP) tensor")
+        W, _ = _matrix(b, "b")
+        G, op = None, None
+        bp, ldb = _arg(b, "b", U8, dev, (W, K))
+        sbp, ldsb = _arg(sb, "sb", F32, dev, (W // 128, K // 128))
     else:
-        _need(offsets, "offsets", I32, None)
-        G = offsets.shape[0] - 1
-        _need(b, "b", U8, G, None, K)
-        R = b.shape[1]
-        _need(sb, "sb", F32, G, R // 128, K // 128)
-        if G < 0 or b.shape[0] != G or not b.is_contiguous() or not sb.is_contiguous() or sb.shape[1] != R // 128:
-            raise ValueError("b and sb must be contiguous [G, 2N, K] / [G, 2N/128, K/128], offsets [G + 1]")
-    if R % 2:
+        if not isinstance(b, torch.Tensor) or b.dim() != 3:
+            raise TypeError("b must be a CUDA (HIP) tensor [G, 2N, K]")
+        G, W, _ = b.shape
+        op, _ = _arg(offsets, "offsets", I32, dev, (G + 1,))
+        bp, _ = _arg(b, "b", U8, dev, (G, W, K))
+        sbp, _ = _arg(sb, "sb", F32, dev, (G, W // 128, K // 128))
+        ldb = ldsb = None
+    if W % 2:
         raise ValueError("b must stack as many up rows as gate rows")
     if accum == ACCUM_MFMA8_POW2:
         flat = sb if G is None else sb.view(-1, sb.shape[2])
-        _check_pow2_mode(accum, sa, M, flat, 0, _ld(flat), 1, flat.shape[0] * 128, K // 128)
-    return M, R // 2, K, G
+        _check_pow2_mode(accum, sa, M, flat, 0, flat.stride(0), 1, flat.shape[0] * 128, K // 128)
+    return M, W // 2, K, G, op, (ap, lda, sap, ldsa, bp, ldb, sbp, ldsb)
 
 
-def _gated_kept(gu, save_gu, M, N, a):
-    if gu is None and save_gu:
-        gu = _new((a.shape[0], 2 * N), BF16, a)
-    if gu is not None:
-        _need(gu, "gu", BF16, M, 2 * N)
-    return gu
-
-
-def _gated_workspace(workspace, M, N, K, a):
-    need = gated_workspace_bytes(M, N, K)
-    if need == 0:
-        return None, 0
-    if workspace is None:
-        workspace = _new((need,), U8, a)
-    _need(workspace, "workspace", U8, None)
-    return workspace, workspace.numel()
+def _kept(gu, save_gu, M, N, dev, like):
+    if gu is None and not save_gu:
+        return None, None, 0
+    return _out(gu, "gu", BF16, dev, (M, 2 * N), like)
 
 
 def fp8_gated_gemm(a, sa, b, sb, act=ACT_SILU, out_dtype=OUT_BF16, d=None, gu=None, save_gu=False, workspace=None,
@@ -136,45 +181,26 @@ def fp8_gated_gemm(a, sa, b, sb, act=ACT_SILU, out_dtype=OUT_BF16, d=None, gu=No
     """H = act(X Wg^T) * (X Wu^T).  a [M, K] codes, sa [K/128, M]; b [2N, K]
     codes (gate rows, then up rows), sb [2N/128, K/128].  Returns (d [M, N],
     gu [M, 2N] bf16 pre-activations or None)."""
-    M, N, K, _ = _gated_operands(a, sa, b, sb, accum)
-    dt = F32 if out_dtype == OUT_F32 else BF16
-    if d is None:
-        d = _new((M, N), dt, a)
-    else:
-        _need(d, "d", dt, M, N)
-    gu = _gated_kept(gu, save_gu, M, N, a)
-    ws, ws_bytes = _gated_workspace(workspace, M, N, K, a)
-    _check(lib().fp8_gated_gemm(M, N, K, _ptr(a), _ld(a), _ptr(sa), _ld(sa), _ptr(b), _ld(b), _ptr(sb), _ld(sb), act,
-                                _ptr(d), _ld(d), out_dtype, _ptr(gu), _ld(gu) if gu is not None else 0, accum,
-                                _ptr(ws), ws_bytes, _stream()), "fp8_gated_gemm")
+    dev = _device(a, "a")
+    M, N, K, _, _, ops = _gated_operands(a, sa, b, sb, accum, dev)
+    d, dp, ldd = _out(d, "d", F32 if out_dtype == OUT_F32 else BF16, dev, (M, N), a)
+    gu, gup, ldgu = _kept(gu, save_gu, M, N, dev, a)
+    ws = _workspace(workspace, gated_workspace_bytes(M, N, K), dev, a)
+    _check(lib().fp8_gated_gemm(M, N, K, *ops, act, dp, ldd, out_dtype, gup, ldgu, accum, *ws, _stream_of(dev)),
+           "fp8_gated_gemm")
     return d, gu
-
-
-def _quant_out(q, s, M, N, a, rows):
-    if q is None:
-        q = _new((rows, N), U8, a)
-    else:
-        _need(q, "q", U8, M, N)
-    if s is None:
-        s = _new((N // 128, rows), F32, a)
-    else:
-        _need(s, "s", F32, N // 128, None)
-        if s.shape[1] < M:
-            raise ValueError(f"s has room for {s.shape[1]} rows' scales, needs {M}")
-    return q, s
 
 
 def fp8_gated_gemm_quant(a, sa, b, sb, act=ACT_SILU, scale_mode=SCALE_FP32, q=None, s=None, gu=None, save_gu=False,
                          workspace=None, accum=ACCUM_FP32):
     """fp8_gated_gemm with H quantised 1x128: returns (q [M, N], s [N/128, M],
     gu or None)."""
-    M, N, K, _ = _gated_operands(a, sa, b, sb, accum)
-    q, s = _quant_out(q, s, M, N, a, M)
-    gu = _gated_kept(gu, save_gu, M, N, a)
-    ws, ws_bytes = _gated_workspace(workspace, M, N, K, a)
-    _check(lib().fp8_gated_gemm_quant(M, N, K, _ptr(a), _ld(a), _ptr(sa), _ld(sa), _ptr(b), _ld(b), _ptr(sb), _ld(sb),
-                                      act, scale_mode, _ptr(q), _ld(q), _ptr(s), _ld(s), _ptr(gu),
-                                      _ld(gu) if gu is not None else 0, accum, _ptr(ws), ws_bytes, _stream()),
+    dev = _device(a, "a")
+    M, N, K, _, _, ops = _gated_operands(a, sa, b, sb, accum, dev)
+    q, s, out = _quant_out(q, s, M, N, dev, a)
+    gu, gup, ldgu = _kept(gu, save_gu, M, N, dev, a)
+    ws = _workspace(workspace, gated_workspace_bytes(M, N, K, True), dev, a)
+    _check(lib().fp8_gated_gemm_quant(M, N, K, *ops, act, scale_mode, *out, gup, ldgu, accum, *ws, _stream_of(dev)),
            "fp8_gated_gemm_quant")
     return q, s, gu
 
@@ -184,59 +210,57 @@ def fp8_grouped_gated_gemm(offsets, a, sa, b, sb, act=ACT_SILU, out_dtype=OUT_BF
     """fp8_gated_gemm over experts: rows offsets[e]..offsets[e+1]-1 of a use
     b[e] [2N, K] and sb[e].  Rows at and after offsets[-1] are left as they
     are.  Returns (d, gu or None)."""
-    M, N, K, G = _gated_operands(a, sa, b, sb, accum, rows_bound, offsets)
-    dt = F32 if out_dtype == OUT_F32 else BF16
-    if d is None:
-        d = _new((M, N), dt, a)
-    else:
-        _need(d, "d", dt, M, N)
-    gu = _gated_kept(gu, save_gu, M, N, a)
-    _check(lib().fp8_grouped_gated_gemm(G, M, N, K, _ptr(offsets), _ptr(a), _ld(a), _ptr(sa), _ld(sa), _ptr(b),
-                                        _ptr(sb), act, _ptr(d), _ld(d), out_dtype, _ptr(gu),
-                                        _ld(gu) if gu is not None else 0, accum, _stream()), "fp8_grouped_gated_gemm")
+    dev = _device(a, "a")
+    M, N, K, G, op, ops = _gated_operands(a, sa, b, sb, accum, dev, rows_bound, offsets)
+    ap, lda, sap, ldsa, bp, _, sbp, _ = ops
+    d, dp, ldd = _out(d, "d", F32 if out_dtype == OUT_F32 else BF16, dev, (M, N), a)
+    gu, gup, ldgu = _kept(gu, save_gu, M, N, dev, a)
+    _check(lib().fp8_grouped_gated_gemm(G, M, N, K, op, ap, lda, sap, ldsa, bp, sbp, act, dp, ldd, out_dtype, gup,
+                                        ldgu, accum, _stream_of(dev)), "fp8_grouped_gated_gemm")
     return d, gu
 
 
 def fp8_grouped_gated_gemm_quant(offsets, a, sa, b, sb, act=ACT_SILU, scale_mode=SCALE_FP32, rows_bound=None, q=None,
                                  s=None, gu=None, save_gu=False, accum=ACCUM_FP32):
     """fp8_gated_gemm_quant over experts; returns (q, s, gu or None)."""
-    M, N, K, G = _gated_operands(a, sa, b, sb, accum, rows_bound, offsets)
-    q, s = _quant_out(q, s, M, N, a, M)
-    gu = _gated_kept(gu, save_gu, M, N, a)
-    _check(lib().fp8_grouped_gated_gemm_quant(G, M, N, K, _ptr(offsets), _ptr(a), _ld(a), _ptr(sa), _ld(sa), _ptr(b),
-                                              _ptr(sb), act, scale_mode, _ptr(q), _ld(q), _ptr(s), _ld(s), _ptr(gu),
-                                              _ld(gu) if gu is not None else 0, accum, _stream()),
-           "fp8_grouped_gated_gemm_quant")
+    dev = _device(a, "a")
+    M, N, K, G, op, ops = _gated_operands(a, sa, b, sb, accum, dev, rows_bound, offsets)
+    ap, lda, sap, ldsa, bp, _, sbp, _ = ops
+    q, s, out = _quant_out(q, s, M, N, dev, a)
+    gu, gup, ldgu = _kept(gu, save_gu, M, N, dev, a)
+    _check(lib().fp8_grouped_gated_gemm_quant(G, M, N, K, op, ap, lda, sap, ldsa, bp, sbp, act, scale_mode, *out, gup,
+                                              ldgu, accum, _stream_of(dev)), "fp8_grouped_gated_gemm_quant")
     return q, s, gu
 
 
-def _gated_backward(name, lead, P, dh, gu, act, scale_mode, qr, sr, qc, sc, qh, sh, with_rows, with_cols, with_h):
-    _need(dh, "dh", BF16, None, None)
+def _gated_backward(name, lead, dev, P, dh, gu, act, scale_mode, rows, cols, h, on):
     M, N = dh.shape
-    _need(gu, "gu", BF16, M, 2 * N)
-    args = []
-    for on, q, s, qn, sn, qshape, sshape in (
-            (with_rows, qr, sr, "qr", "sr", (M, 2 * N), (2 * N // 128, M)),
-            (with_cols, qc, sc, "qc", "sc", (2 * N, P), (P // 128, 2 * N)),
-            (with_h, qh, sh, "qh", "sh", (N, P), (P // 128, N))):
-        if not on:
-            args.append((None, None))
+    dhp, lddh = _arg(dh, "dh", BF16, dev, (M, N))
+    gup, ldgu = _arg(gu, "gu", BF16, dev, (M, 2 * N), True)
+    outs, args = [], []
+    for (q, s), (qn, sn), R, C, wanted in ((rows, ("qr", "sr"), M, 2 * N, on[0]), (cols, ("qc", "sc"), 2 * N, P, on[1]),
+                                           (h, ("qh", "sh"), N, P, on[2])):
+        if not wanted:
+            outs += [None, None]
+            args += [None, 0, None, 0]
             continue
+        # codes [R, >= C]; scales [C/128, R] of rows, [C/128, R] on the padded row axis alike
         if q is None:
-            q = _new(qshape, U8, dh)
+            q = torch.empty((R, C), dtype=U8, device=dh.device)
         if s is None:
-            s = _new(sshape, F32, dh)
-        _need(q, qn, U8, qshape[0], None)
-        _need(s, sn, F32, sshape[0], None)
-        if q.shape[1] < qshape[1] or s.shape[1] < sshape[1]:
-            raise ValueError(f"{qn} and {sn} need {qshape} and {sshape}, got {tuple(q.shape)} and {tuple(s.shape)}")
-        args.append((q, s))
-    flat = []
-    for q, s in args:
-        flat += [_ptr(q), _ld(q) if q is not None else 0, _ptr(s), _ld(s) if s is not None else 0]
-    _check(getattr(lib(), name)(*lead, M, N, _ptr(dh), _ld(dh), _ptr(gu), _ld(gu), act, scale_mode, *flat, _stream()),
-           name)
-    return tuple(t for pair in args for t in pair)
+            s = torch.empty((C // 128, R), dtype=F32, device=dh.device)
+        if q.dim() == 2 and q.shape[1] > C:
+            qp, ldq = _arg(q, qn, U8, dev, (R, None), True)
+        else:
+            qp, ldq = _arg(q, qn, U8, dev, (R, C), True)
+        if s.dim() == 2 and s.shape[1] > R:
+            sp, lds = _arg(s, sn, F32, dev, (C // 128, None), True)
+        else:
+            sp, lds = _arg(s, sn, F32, dev, (C // 128, R), True)
+        outs += [q, s]
+        args += [qp, ldq, sp, lds]
+    _check(getattr(lib(), name)(*lead, M, N, dhp, lddh, gup, ldgu, act, scale_mode, *args, _stream_of(dev)), name)
+    return tuple(outs)
 
 
 def fp8_gated_backward(dh, gu, act=ACT_SILU, scale_mode=SCALE_FP32, qr=None, sr=None, qc=None, sc=None, qh=None,
@@ -245,9 +269,10 @@ def fp8_gated_backward(dh, gu, act=ACT_SILU, scale_mode=SCALE_FP32, qr=None, sr=
     (bf16).  Returns (qr, sr, qc, sc, qh, sh): dG | dU in 1x128 groups
     [M, 2N], in 128x1 groups [2N, P] and H in 128x1 groups [N, P], P = M
     rounded up to 128; None for those switched off."""
-    P = (dh.shape[0] + 127) // 128 * 128
-    return _gated_backward("fp8_gated_backward", (), P, dh, gu, act, scale_mode, qr, sr, qc, sc, qh, sh,
-                           with_rows, with_cols, with_h)
+    dev = _device(dh, "dh")
+    M, _ = _matrix(dh, "dh")
+    return _gated_backward("fp8_gated_backward", (), dev, (M + 127) // 128 * 128, dh, gu, act, scale_mode, (qr, sr),
+                           (qc, sc), (qh, sh), (with_rows, with_cols, with_h))
 
 
 def fp8_grouped_gated_backward(offsets, dh, gu, act=ACT_SILU, scale_mode=SCALE_FP32, qr=None, sr=None, qc=None,
@@ -256,13 +281,13 @@ def fp8_grouped_gated_backward(offsets, dh, gu, act=ACT_SILU, scale_mode=SCALE_F
     expert, on the padded axis of fp8_quant_tile_grouped_col (P =
     grouped_col_bound(M, G); what lies past the last group is left as it
     is)."""
-    _need(offsets, "offsets", I32, None)
-    G = offsets.shape[0] - 1
-    if G < 0:
+    dev = _device(dh, "dh")
+    M, _ = _matrix(dh, "dh")
+    op, n = _arg(offsets, "offsets", I32, dev, (None,))
+    if n < 1:
         raise ValueError("offsets must have at least one entry")
-    P = grouped_col_bound(dh.shape[0], G)
-    return _gated_backward("fp8_grouped_gated_backward", (G, _ptr(offsets)), P, dh, gu, act, scale_mode, qr, sr, qc,
-                           sc, qh, sh, with_rows, with_cols, with_h)
+    return _gated_backward("fp8_grouped_gated_backward", (n - 1, op), dev, grouped_col_bound(M, n - 1), dh, gu, act,
+                           scale_mode, (qr, sr), (qc, sc), (qh, sh), (with_rows, with_cols, with_h))
 
 
 # ---- norms ---------------------------------------------------------------------------
@@ -271,24 +296,20 @@ NormResidual = collections.namedtuple("NormResidual", "xo h q s rstd_y rstd_x")
 NormResidualGrads = collections.namedtuple("NormResidualGrads", "dx dy dw_pre dw_post dgate")
 
 
-def _seam_inputs(M, D, y, w_post, gate, gate_rows, w_pre):
-    if y is not None:
-        _need(y, "y", BF16, M, D)
-        if y.shape[0] != M:
-            raise ValueError(f"y has {y.shape[0]} rows, x has {M}")
-    if w_post is not None:
-        _need(w_post, "w_post", F32, D)
-    if w_pre is not None:
-        _need(w_pre, "w_pre", F32, D)
+def _seam(M, D, dev, y, w_post, gate, gate_rows):
+    """Addresses and leading dimensions of the residual sum's inputs: (y, ldy,
+    w_post, gate, gate_rows)."""
+    yp, ldy = _arg(y, "y", BF16, dev, (M, D)) if y is not None else (None, 0)
+    wp = _arg(w_post, "w_post", F32, dev, (D,))[0] if w_post is not None else None
     if gate is None:
-        return 0
+        return yp, ldy, wp, None, 0
     rows = max(M, 1) if gate_rows is None else int(gate_rows)
     if rows < 1:
         raise ValueError(f"gate_rows must be at least 1, got {rows}")
-    _need(gate, "gate", F32, (M + rows - 1) // rows, D)
-    if not gate.is_contiguous():
+    gp, ldg = _arg(gate, "gate", F32, dev, ((M + rows - 1) // rows, D))
+    if gate.shape[0] > 1 and ldg != D:
         raise ValueError("gate must be contiguous")
-    return rows
+    return yp, ldy, wp, gp, rows
 
 
 def fp8_norm_residual(x, w_pre=None, y=None, w_post=None, gate=None, gate_rows=None, alpha=1.0, eps=1e-6,
@@ -298,28 +319,26 @@ def fp8_norm_residual(x, w_pre=None, y=None, w_post=None, gate=None, gate_rows=N
     w_pre, w_post fp32 [D]; gate fp32 [ceil(M/gate_rows), D] (gate_rows None:
     one row for all).  Returns NormResidual(xo, h, q, s, rstd_y, rstd_x), None
     for what was not asked for."""
-    _need(x, "x", BF16, None, None)
-    M, D = x.shape
-    rows = _seam_inputs(M, D, y, w_post, gate, gate_rows, w_pre)
-    quantise = w_pre is not None and (quantise or q is not None)
+    dev = _device(x, "x")
+    M, D = _matrix(x, "x")
+    xp, ldx = _arg(x, "x", BF16, dev, (M, D))
+    yp, ldy, wp, gp, rows = _seam(M, D, dev, y, w_post, gate, gate_rows)
+    xop, ldxo, hp, ldh, out, prep = None, 0, None, 0, (None, 0, None, 0), None
     if y is not None:
-        if xo is None:
-            xo = _new((M, D), BF16, x)
-        else:
-            _need(xo, "xo", BF16, M, D)
-    if quantise:
-        q, s = _quant_out(q, s, M, D, x, M)
-    if want_h and h is None:
-        h = _new((M, D), BF16, x)
-    if h is not None:
-        _need(h, "h", BF16, M, D)
-    ry = _new((M,), F32, x) if w_post is not None else None
-    rx = _new((M,), F32, x) if w_pre is not None else None
-    _check(lib().fp8_norm_residual(M, D, _ptr(x), _ld(x), _ptr(y), _ld(y) if y is not None else 0, _ptr(w_post),
-                                   _ptr(gate), rows, alpha, eps, _ptr(xo), _ld(xo) if xo is not None else 0,
-                                   _ptr(w_pre), _ptr(h), _ld(h) if h is not None else 0, scale_mode, _ptr(q),
-                                   _ld(q) if q is not None else 0, _ptr(s), _ld(s) if s is not None else 0, _ptr(ry),
-                                   _ptr(rx), _stream()), "fp8_norm_residual")
+        xo, xop, ldxo = _out(xo, "xo", BF16, dev, (M, D), x)
+    # the statistics in one allocation
+    stats = torch.empty((2, M), dtype=F32, device=x.device)
+    ry, rx = stats[0] if w_post is not None else None, None
+    if w_pre is not None:
+        prep = _arg(w_pre, "w_pre", F32, dev, (D,))[0]
+        rx = stats[1]
+        if quantise or q is not None:
+            q, s, out = _quant_out(q, s, M, D, dev, x)
+        if want_h or h is not None:
+            h, hp, ldh = _out(h, "h", BF16, dev, (M, D), x)
+    _check(lib().fp8_norm_residual(M, D, xp, ldx, yp, ldy, wp, gp, rows, alpha, eps, xop, ldxo, prep, hp, ldh,
+                                   scale_mode, *out, ry.data_ptr() if ry is not None else None,
+                                   rx.data_ptr() if rx is not None else None, _stream_of(dev)), "fp8_norm_residual")
     return NormResidual(xo, h, q, s, ry, rx)
 
 
@@ -328,67 +347,55 @@ def fp8_norm_residual_backward(dxo, dh, xo, rstd_x, w_pre, y=None, rstd_y=None, 
     """Gradients of fp8_norm_residual from dxo (of x', or None) and dh (of
     RMSNorm(x') w_pre, or None), bf16 [M, D].  Returns NormResidualGrads(dx,
     dy, dw_pre, dw_post, dgate), None where the input was None."""
-    lead = dxo if dxo is not None else dh
-    _need(lead, "dxo" if dxo is not None else "dh", BF16, None, None)
-    M, D = lead.shape
+    lead, name = (dxo, "dxo") if dxo is not None else (dh, "dh")
+    dev = _device(lead, name)
+    M, D = _matrix(lead, name)
+    dxop, lddxo = _arg(dxo, "dxo", BF16, dev, (M, D)) if dxo is not None else (None, 0)
+    dhp = rxp = prep = xop = None
+    lddh = ldxo = 0
     if dh is not None:
-        for t, name in ((dh, "dh"), (xo, "xo")):
-            _need(t, name, BF16, M, D)
-        _need(rstd_x, "rstd_x", F32, M)
-        _need(w_pre, "w_pre", F32, D)
-    rows = _seam_inputs(M, D, y, w_post, gate, gate_rows, None)
-    if w_post is not None:
-        _need(rstd_y, "rstd_y", F32, M)
-    if dx is None:
-        dx = _new((M, D), BF16, lead)
-    else:
-        _need(dx, "dx", BF16, M, D)
+        dhp, lddh = _arg(dh, "dh", BF16, dev, (M, D))
+        xop, ldxo = _arg(xo, "xo", BF16, dev, (M, D))
+        rxp = _arg(rstd_x, "rstd_x", F32, dev, (M,))[0]
+        prep = _arg(w_pre, "w_pre", F32, dev, (D,))[0]
+    yp, ldy, wp, gp, rows = _seam(M, D, dev, y, w_post, gate, gate_rows)
+    ryp = _arg(rstd_y, "rstd_y", F32, dev, (M,))[0] if w_post is not None else None
+    dx, dxp, lddx = _out(dx, "dx", BF16, dev, (M, D), lead)
+    dyp, lddy = None, 0
     if y is not None:
-        if dy is None:
-            dy = _new((M, D), BF16, lead)
-        else:
-            _need(dy, "dy", BF16, M, D)
-    dw_pre = _new((D,), F32, lead) if dh is not None else None
-    dw_post = _new((D,), F32, lead) if w_post is not None else None
+        dy, dyp, lddy = _out(dy, "dy", BF16, dev, (M, D), lead)
+    dw = torch.empty((2, D), dtype=F32, device=lead.device)
+    dw_pre, dw_post = dw[0] if dh is not None else None, dw[1] if w_post is not None else None
     dgate = torch.empty_like(gate) if gate is not None else None
-    need = int(lib().fp8_norm_backward_workspace_bytes(M, D))
-    if workspace is None:
-        workspace = _new((need,), U8, lead)
-    _need(workspace, "workspace", U8, None)
-    ld = lambda t: _ld(t) if t is not None else 0  # noqa: E731
-    _check(lib().fp8_norm_residual_backward(
-        M, D, _ptr(dxo), ld(dxo), _ptr(dh), ld(dh), _ptr(xo) if dh is not None else None, ld(xo) if dh is not None else 0,
-        _ptr(rstd_x) if dh is not None else None, _ptr(w_pre) if dh is not None else None, _ptr(y), ld(y),
-        _ptr(rstd_y) if w_post is not None else None, _ptr(w_post), _ptr(gate), rows, alpha, _ptr(dx), ld(dx), _ptr(dy),
-        ld(dy), _ptr(dw_pre), _ptr(dw_post), _ptr(dgate), _ptr(workspace), workspace.numel(), _stream()),
-        "fp8_norm_residual_backward")
+    ws = _workspace(workspace, lib().fp8_norm_backward_workspace_bytes(M, D), dev, lead)
+    _check(lib().fp8_norm_residual_backward(M, D, dxop, lddxo, dhp, lddh, xop, ldxo, rxp, prep, yp, ldy, ryp, wp, gp,
+                                            rows, alpha, dxp, lddx, dyp, lddy, _ptr(dw_pre), _ptr(dw_post),
+                                            _ptr(dgate), *ws, _stream_of(dev)), "fp8_norm_residual_backward")
     return NormResidualGrads(dx, dy, dw_pre, dw_post, dgate)
 
 
 # ---- gradient norm and clipping -------------------------------------------------------
 
 def _grad_table(grads, name):
-    """(pointers, counts, types) as host arrays of the C ABI."""
-    n = len(grads)
-    ptr, count, dtype = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)(), (ctypes.c_int32 * n)()
-    here = torch.cuda.current_device()
-    for i, g in enumerate(grads):
-        if not isinstance(g, torch.Tensor) or not g.is_cuda or g.get_device() != here:
-            raise TypeError(f"{name}[{i}] must be a CUDA (HIP) tensor on the current device")
-        if g.dtype is not F32 and g.dtype is not BF16:
-            raise TypeError(f"{name}[{i}] must be float32 or bfloat16, got {g.dtype}")
-        if not g.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be contiguous")
-        ptr[i], count[i], dtype[i] = g.data_ptr(), g.numel(), OUT_F32 if g.dtype is F32 else OUT_BF16
-    return ptr, count, dtype
+    """(addresses, counts, types) of the gradients as lists."""
+    if not all([isinstance(g, torch.Tensor) and g.is_cuda for g in grads]):
+        raise TypeError(f"every tensor of {name} must be a CUDA (HIP) tensor")
+    dev = torch.cuda.current_device()
+    if not all([g.get_device() == dev for g in grads]):
+        raise ValueError(f"every tensor of {name} must be on the current device, cuda:{dev}")
+    dtypes = [g.dtype for g in grads]
+    if not all(t is F32 or t is BF16 for t in dtypes):
+        raise TypeError(f"{name} must be float32 or bfloat16, got {set(dtypes)}")
+    if not all([g.is_contiguous() for g in grads]):
+        raise ValueError(f"every tensor of {name} must be contiguous")
+    return [g.data_ptr() for g in grads], [g.numel() for g in grads], [OUT_F32 if t is F32 else OUT_BF16
+                                                                       for t in dtypes]
 
 
-def _grad_workspace(n, workspace):
-    need = int(lib().fp8_grad_workspace_bytes(n))
-    if workspace is None:
-        workspace = torch.empty(need, dtype=U8, device="cuda")
-    _need(workspace, "workspace", U8, None)
-    return workspace
+def _host(values, code):
+    """A host array for the C ABI: the array (which owns the memory) and its address."""
+    a = array.array(code, values)
+    return a, a.buffer_info()[0]
 
 
 def fp8_grad_norm(grads, workspace=None):
@@ -396,10 +403,11 @@ def fp8_grad_norm(grads, workspace=None):
     one-element fp32 tensor on the device."""
     grads = list(grads)
     ptr, count, dtype = _grad_table(grads, "grads")
-    ws = _grad_workspace(len(grads), workspace)
+    dev = torch.cuda.current_device()
+    (p, pp), (c, cp), (t, tp) = _host(ptr, "Q"), _host(count, "q"), _host(dtype, "i")
     norm = torch.empty(1, dtype=F32, device="cuda")
-    _check(lib().fp8_grad_norm(len(grads), ptr, count, dtype, _ptr(norm), _ptr(ws), ws.numel(), _stream()),
-           "fp8_grad_norm")
+    ws = _workspace(workspace, lib().fp8_grad_workspace_bytes(len(grads)), dev, norm)
+    _check(lib().fp8_grad_norm(len(grads), pp, cp, tp, norm.data_ptr(), *ws, _stream_of(dev)), "fp8_grad_norm")
     return norm
 
 
@@ -408,14 +416,17 @@ def fp8_grad_clip(grads, max_norm, out=None, workspace=None):
     into `out` (tensors of the same types and sizes).  Returns (norm, coef),
     one-element fp32 tensors on the device."""
     grads = list(grads)
-    out = grads if out is None else list(out)
     ptr, count, dtype = _grad_table(grads, "grads")
-    optr, ocount, odtype = (ptr, count, dtype) if out is grads else _grad_table(out, "out")
-    if len(out) != len(grads) or list(ocount) != list(count) or list(odtype) != list(dtype):
-        raise ValueError("out must match grads in number, sizes and types")
-    ws = _grad_workspace(len(grads), workspace)
+    dev = torch.cuda.current_device()
+    optr = ptr
+    if out is not None:
+        optr, ocount, odtype = _grad_table(list(out), "out")
+        if ocount != count or odtype != dtype:
+            raise ValueError("out must match grads in number, sizes and types")
+    (p, pp), (c, cp), (t, tp), (o, op) = _host(ptr, "Q"), _host(count, "q"), _host(dtype, "i"), _host(optr, "Q")
     res = torch.empty(2, dtype=F32, device="cuda")
-    norm, coef = res[:1], res[1:]
-    _check(lib().fp8_grad_clip(len(grads), ptr, count, dtype, float(max_norm), optr, _ptr(norm), _ptr(coef), _ptr(ws),
-                               ws.numel(), _stream()), "fp8_grad_clip")
-    return norm, coef
+    ws = _workspace(workspace, lib().fp8_grad_workspace_bytes(len(grads)), dev, res)
+    at = res.data_ptr()
+    _check(lib().fp8_grad_clip(len(grads), pp, cp, tp, float(max_norm), op, at, at + 4, *ws, _stream_of(dev)),
+           "fp8_grad_clip")
+    return res[:1], res[1:]

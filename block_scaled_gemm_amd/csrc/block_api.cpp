@@ -92,12 +92,12 @@ void set_out_quant(fp8bs::GatedArgs& g, int scale_mode, uint8_t* q, int64_t ldq,
 
 int run_dense(fp8bs::GatedArgs& g, void* workspace, size_t workspace_bytes, void* stream) {
     if (g.M == 0 || g.N == 0) return FP8BS_OK;
-    if ((g.M + 63) / 64 > kMaxGrid / (g.N / 128)) return FP8BS_ERR_SHAPE;
-    const size_t need = fp8bs::gated_workspace(g.M, g.N, g.K);
+    if ((g.M + 31) / 32 > kMaxGrid / (g.N / 8)) return FP8BS_ERR_SHAPE;
+    const size_t need = fp8bs::gated_workspace(g.M, g.N, g.K, g.out >= fp8bs::GATED_QUANT);
     if (need > 0 && (!workspace || workspace_bytes < need)) return FP8BS_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 16)) return FP8BS_ERR_ALIGN;
     if (int r = check_device()) return r;
-    g.splits = need > 0 ? fp8bs::gated_splits(g.M, g.N, g.K) : 1;
+    g.splits = fp8bs::gated_splits(g.M, g.N, g.K);
     g.ws = (float*)workspace;
     return hip_status(fp8bs::launch_gated(g, (hipStream_t)stream));
 }
@@ -120,9 +120,9 @@ int check_offsets(int G, const int32_t* offsets) {
 
 }  // namespace
 
-FP8BS_EXPORT size_t fp8_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (M <= 0 || N <= 0 || K <= 0 || N % 128 != 0 || K % 128 != 0) return 0;
-    return fp8bs::gated_workspace(M, N, K);
+FP8BS_EXPORT size_t fp8_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, int quant) {
+    if (M <= 0 || N <= 0 || K < 0 || N % 128 != 0 || K % 128 != 0) return 0;
+    return fp8bs::gated_workspace(M, N, K, quant != 0);
 }
 
 FP8BS_EXPORT int fp8_gated_gemm(int64_t M, int64_t N, int64_t K, const uint8_t* a, int64_t lda, const float* sa,

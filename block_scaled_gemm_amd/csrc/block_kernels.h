@@ -33,7 +33,7 @@ struct GatedArgs {
     uint16_t* gu;  // optional: the pre-activations, bf16 [M][ldgu], gate | up
     int64_t ldgu;
     int accum;
-    float* ws;  // split-K partials [splits][M][2N]
+    float* ws;  // split-K partials [splits][M][2N], or H of few rows [M][N]
     int splits;
     const int32_t* offsets;  // grouped: device [G+1]
     int G;
@@ -41,7 +41,7 @@ struct GatedArgs {
 };
 
 int gated_splits(int64_t M, int64_t N, int64_t K);
-size_t gated_workspace(int64_t M, int64_t N, int64_t K);
+size_t gated_workspace(int64_t M, int64_t N, int64_t K, bool quant);
 hipError_t launch_gated(const GatedArgs& g, hipStream_t st);
 hipError_t launch_grouped_gated(const GatedArgs& g, hipStream_t st);
 

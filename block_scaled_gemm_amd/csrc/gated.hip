@@ -764,19 +764,141 @@ __global__ __launch_bounds__(256) void gated_reduce_kernel(GatedArgs p) {
     }
 }
 
+// ==== forward: few rows ======================================================================
+//
+// At most 16 rows the product is bound by reading the weights once.  A
+// workgroup takes 8 columns -- one 16-row fragment of 8 gate and 8 up rows --
+// and its eight waves share out the K groups, each loading its fragments
+// straight into registers, all U groups' loads before the first product.  The
+// waves' sums meet in LDS in wave order.  Lane l holds chunks l/16 and 4 + l/16
+// of its row (either operand alike, so equal k meet), so that a load reads 64
+// B runs.
+//
+// Every workgroup reads all of X, so this pays while X stays small next to 8
+// columns' weights: 2N x K = 36864 x 7168 with 1, 4, 16 rows 47, 53, 72 us
+// (5.6 TB/s for one), the 64-row tile 56 us for all of them; 16384 x 7168 with 16
+// rows 31 us.  One row of 4096 x 7168: 8 us, 3.6 TB/s, against 14 for the tiles
+// with K split.
+constexpr int FEW_COLS = 8;
+bool few_rows(int64_t M, int64_t N) { return M <= 16 && M * N <= 131072; }
+
+__device__ __forceinline__ v8i chunks2(const uint8_t* p) {
+    const uint4 lo = *(const uint4*)p, hi = *(const uint4*)(p + 64);
+    v8i r;
+    r[0] = (int)lo.x; r[1] = (int)lo.y; r[2] = (int)lo.z; r[3] = (int)lo.w;
+    r[4] = (int)hi.x; r[5] = (int)hi.y; r[6] = (int)hi.z; r[7] = (int)hi.w;
+    return r;
+}
+
+// The group's partial of a 16 x 16 tile with exact products and fp32 sums.
+__device__ __forceinline__ v4f f16_group(const v8i& b, const v8i& a) {
+    v4f p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const uint4 bw = make_uint4(b[4 * k], b[4 * k + 1], b[4 * k + 2], b[4 * k + 3]);
+        const uint4 aw = make_uint4(a[4 * k], a[4 * k + 1], a[4 * k + 2], a[4 * k + 3]);
+        v8h b0, b1, a0, a1;
+        widen16(bw, b0, b1);
+        widen16(aw, a0, a1);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(b0, a0, p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_f16(b1, a1, p, 0, 0, 0);
+    }
+    return p;
+}
+
+template <int ACC>
+__global__ __launch_bounds__(THREADS) void gated_few_kernel(GatedArgs p) {
+    constexpr int U = 4;
+    __shared__ float sums[WAVES][64][4 + 1];
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int r = lane & 15, q = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * FEW_COLS;
+    const int64_t groups = p.K / 128;
+    const uint8_t* b = p.b + (n0 + (r & 7) + (r < 8 ? 0 : p.N)) * p.ldb + 16 * q;
+    const int64_t row = r < p.M ? r : p.M - 1;
+    const uint8_t* a = p.a + row * p.lda + 16 * q;
+    const float* sa = p.sa + row;
+    const float* sg = p.sb + (n0 >> 7) * p.ldsb;
+    const float* su = sg + (p.N >> 7) * p.ldsb;
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    for (int64_t g0 = wave; g0 < groups; g0 += WAVES * U) {
+        v8i bf[U], af[U];
+        float ss[U], sm[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            // groups past the end load the last one again and are not summed
+            const int64_t g = g0 + u * WAVES < groups ? g0 + u * WAVES : groups - 1;
+            bf[u] = chunks2(b + g * 128);
+            af[u] = chunks2(a + g * 128);
+            // results: lanes 0..31 hold gate columns, 32..63 up; scale
+            // operands of the scaled MFMA go by the fragment's row instead
+            ss[u] = (ACC == 2 ? r >= 8 : q >= 2) ? su[g] : sg[g];
+            sm[u] = sa[g * p.ldsa];
+        }
+        __builtin_amdgcn_sched_barrier(0);  // every load before the first product
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (g0 + u * WAVES >= groups) break;  // wave-uniform
+            if constexpr (ACC == 2)
+                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[u], af[u], acc, 0, 0, 0, e8m0(ss[u]), 0,
+                                                                   e8m0(sm[u]));
+            else
+                acc += (ACC == 1 ? mfma8_group(bf[u], af[u]) : f16_group(bf[u], af[u])) * (sm[u] * ss[u]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e++) sums[wave][lane][e] = acc[e];
+    __syncthreads();
+    // thread: row t / 8, column t % 8
+    const int m = t >> 3, c = t & 7;
+    if (m >= p.M) return;
+    const int at = (c >> 2) * 16 + m;
+    float g = 0.f, u = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; w++) {
+        g += sums[w][at][c & 3];
+        u += sums[w][at + 32][c & 3];
+    }
+    const int64_t n = n0 + c;
+    if (p.gu) {
+        p.gu[m * p.ldgu + n] = (uint16_t)pk_bf16(g, g);
+        p.gu[m * p.ldgu + p.N + n] = (uint16_t)pk_bf16(u, u);
+    }
+    const float h = gated(p.act, g, u);
+    if (p.out == GATED_BF16)
+        ((uint16_t*)p.d)[m * p.ldd + n] = (uint16_t)pk_bf16(h, h);
+    else if (p.out == GATED_F32)
+        ((float*)p.d)[m * p.ldd + n] = h;
+    else
+        p.ws[m * p.N + n] = h;  // a group's other columns are other workgroups': quantised next
+}
+
+// H of few rows from the workspace, quantised.  32 lanes hold a group.
+__global__ __launch_bounds__(256) void gated_few_quant_kernel(GatedArgs p) {
+    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (idx >= p.M * (p.N / 4)) return;  // a multiple of 32: groups are whole or out
+    const int64_t m = idx / (p.N / 4), n = idx % (p.N / 4) * 4;
+    const float4 v = *(const float4*)(p.ws + m * p.N + n);
+    const GroupScale gs = group_scale(group32_amax(v.x, v.y, v.z, v.w), p.out == GATED_QUANT_POW2);
+    *(uint32_t*)((uint8_t*)p.d + m * p.ldd + n) = pack4(v.x * gs.inv, v.y * gs.inv, v.z * gs.inv, v.w * gs.inv);
+    if ((n & 127) == 0) p.qs[(n >> 7) * p.qlds + m] = gs.s;
+}
+
 // ==== forward: host side =====================================================================
 
 // Splits of K where the 128 x 128-column tiles would leave most CUs idle:
 // about one workgroup per CU, at least eight groups a split.
 int gated_splits(int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = ((M + 127) / 128) * (N / 128), groups = K / 128;
+    if (few_rows(M, N)) return 1;
     if (tiles == 0 || groups < 16 || tiles >= 128) return 1;
     int64_t s = 256 / tiles;
     if (s > groups / 8) s = groups / 8;
     return s < 2 ? 1 : (int)s;
 }
 
-size_t gated_workspace(int64_t M, int64_t N, int64_t K) {
+size_t gated_workspace(int64_t M, int64_t N, int64_t K, bool quant) {
+    if (few_rows(M, N)) return quant ? (size_t)M * (size_t)N * sizeof(float) : 0;
     const int s = gated_splits(M, N, K);
     return s <= 1 ? 0 : (size_t)s * (size_t)M * (size_t)(2 * N) * sizeof(float);
 }
@@ -790,6 +912,10 @@ static void launch_gated_shape(const GatedArgs& g, hipStream_t st) {
 
 template <int ACC>
 static void launch_gated_acc(const GatedArgs& g, hipStream_t st) {
+    if (few_rows(g.M, g.N)) {
+        hipLaunchKernelGGL(gated_few_kernel<ACC>, dim3((unsigned)(g.N / FEW_COLS)), dim3(THREADS), 0, st, g);
+        return;
+    }
     if constexpr (ACC == 0) {
         if (g.M <= Shape<23>::BM)
             launch_gated_shape<0, 23>(g, st);
@@ -813,9 +939,14 @@ hipError_t launch_gated(const GatedArgs& g, hipStream_t st) {
         launch_gated_acc<1>(g, st);
     else
         launch_gated_acc<2>(g, st);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || g.splits <= 1) return e;
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     const int64_t n = g.M * (g.N / 4);
+    if (few_rows(g.M, g.N) && g.out >= GATED_QUANT) {
+        hipLaunchKernelGGL(gated_few_quant_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, g);
+        return hipGetLastError();
+    }
+    if (g.splits <= 1) return e;
     hipLaunchKernelGGL(gated_reduce_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, g);
     return hipGetLastError();
 }

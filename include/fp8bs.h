@@ -505,7 +505,7 @@ int fp8_grouped_gemm_strided(int G, int64_t rows_bound, int64_t N, int64_t K,
  *           pass).
  *   accum   one of FP8BS_ACCUM_*.  The product is formed from the FP32
  *           accumulators; an error of G or U enters D through act' and act.
- *   workspace  device scratch of fp8_gated_workspace_bytes(M, N, K) bytes
+ *   workspace  device scratch of fp8_gated_workspace_bytes(M, N, K, 0) bytes
  *           (may be NULL when that is 0), for partial sums over K where there
  *           are few rows.  Two calls that may run at the same time, two
  *           captured graphs among them, need one each.
@@ -525,16 +525,16 @@ int fp8_gated_gemm(int64_t M, int64_t N, int64_t K, const uint8_t *a,
                    uint16_t *gu, int64_t ldgu, int accum, void *workspace,
                    size_t workspace_bytes, void *stream);
 
-/* Workspace bytes fp8_gated_gemm and fp8_gated_gemm_quant need for this shape
- * (0 = none). */
-size_t fp8_gated_workspace_bytes(int64_t M, int64_t N, int64_t K);
+/* Workspace bytes fp8_gated_gemm (quant 0) or fp8_gated_gemm_quant (quant 1)
+ * needs for this shape (0 = none). */
+size_t fp8_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, int quant);
 
 /*
  * fp8_gated_gemm_quant -- fp8_gated_gemm with H quantised in 1x128 groups
  * along n, ready for the down-projection: q codes [M][ldq], s[g*lds + m] the
  * scale of row m, columns 128g .. 128g+127.  Scale and codes come from the
  * fp32 product in one rounding (no bf16 rounding between, unlike
- * fp8_gemm_blockscaled_quant).
+ * fp8_gemm_blockscaled_quant).  Workspace: fp8_gated_workspace_bytes(M, N, K, 1).
  * Alignment: q 4-byte aligned, ldq a multiple of 4; s 4-byte aligned;
  * ldq >= N; lds >= M; otherwise as fp8_gated_gemm.
  */

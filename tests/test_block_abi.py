@@ -51,9 +51,14 @@ def test_gated_gemm_quant(kw, want):
 
 
 def test_gated_workspace_query():
-    assert bs.gated_workspace_bytes(4096, 18432, 7168) == 0
-    assert bs.gated_workspace_bytes(1, 2048, 7168) >= 2 * 4096 * 4
-    assert bs.gated_workspace_bytes(1, 100, 7168) == 0 and bs.gated_workspace_bytes(0, 2048, 7168) == 0
+    for quant in (False, True):
+        assert bs.gated_workspace_bytes(4096, 18432, 7168, quant) == 0
+        assert bs.gated_workspace_bytes(100, 2048, 7168, quant) >= 2 * 100 * 4096 * 4
+        assert bs.gated_workspace_bytes(100, 100, 7168, quant) == 0
+        assert bs.gated_workspace_bytes(0, 2048, 7168, quant) == 0
+    # a few rows' H waits there for its groups
+    assert bs.gated_workspace_bytes(3, 2048, 7168) == 0
+    assert bs.gated_workspace_bytes(3, 2048, 7168, True) == 3 * 2048 * 4
 
 
 GROUPED = dict(G=4, rows=64, N=256, K=512, off=FAKE, a=FAKE, lda=512, sa=FAKE, ldsa=64, b=FAKE, sb=FAKE, act=0,
