@@ -377,19 +377,21 @@ def fp8_norm_residual_backward(dxo, dh, xo, rstd_x, w_pre, y=None, rstd_y=None, 
 # ---- gradient norm and clipping -------------------------------------------------------
 
 def _grad_table(grads, name):
-    """(addresses, counts, types) of the gradients as lists."""
-    if not all([isinstance(g, torch.Tensor) and g.is_cuda for g in grads]):
+    """(addresses, counts, types) of the gradients as lists.  Many small
+    tensors make this most of the call: one pass per attribute, no Python
+    frame per tensor."""
+    T = torch.Tensor
+    devices = set(map(T.get_device, grads))  # -1: host memory (no tensor at all: TypeError)
+    if -1 in devices:
         raise TypeError(f"every tensor of {name} must be a CUDA (HIP) tensor")
-    dev = torch.cuda.current_device()
-    if not all([g.get_device() == dev for g in grads]):
-        raise ValueError(f"every tensor of {name} must be on the current device, cuda:{dev}")
+    if devices and devices != {torch.cuda.current_device()}:
+        raise ValueError(f"every tensor of {name} must be on the current device")
     dtypes = [g.dtype for g in grads]
-    if not all(t is F32 or t is BF16 for t in dtypes):
+    if not set(dtypes) <= {F32, BF16}:
         raise TypeError(f"{name} must be float32 or bfloat16, got {set(dtypes)}")
-    if not all([g.is_contiguous() for g in grads]):
+    if not all(map(T.is_contiguous, grads)):
         raise ValueError(f"every tensor of {name} must be contiguous")
-    return [g.data_ptr() for g in grads], [g.numel() for g in grads], [OUT_F32 if t is F32 else OUT_BF16
-                                                                       for t in dtypes]
+    return list(map(T.data_ptr, grads)), list(map(T.numel, grads)), [t is F32 for t in dtypes]
 
 
 def _host(values, code):
