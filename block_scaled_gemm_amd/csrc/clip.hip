@@ -18,6 +18,27 @@ namespace fp8bs {
 
 constexpr int CT = 512;
 
+// 16-byte accesses, eight of a thread's in flight, non-temporal: the gradients
+// pass through once per kernel (940M fp32 elements: one in flight 2067 us,
+// eight 1940 us for both kernels, 5.8 TB/s over the three passes).
+constexpr int CU = 8;
+typedef uint32_t u32x4_c __attribute__((ext_vector_type(4)));
+
+// f(k, v[k]) for the 16-byte vectors v[0..n) of p, shared out over the workgroup.
+template <typename F>
+__device__ __forceinline__ void each16(const void* p, int n, F f) {
+    const u32x4_c* v = (const u32x4_c*)p;
+    int k = threadIdx.x;
+    for (; k + (CU - 1) * CT < n; k += CU * CT) {
+        u32x4_c w[CU];
+#pragma unroll
+        for (int j = 0; j < CU; j++) w[j] = __builtin_nontemporal_load(v + k + j * CT);
+#pragma unroll
+        for (int j = 0; j < CU; j++) f(k + j * CT, w[j]);
+    }
+    for (; k < n; k += CT) f(k, __builtin_nontemporal_load(v + k));
+}
+
 // The tensor that chunk c of the launch belongs to.
 __device__ __forceinline__ int chunk_tensor(const ClipTable& t, int c) {
     int lo = 0, hi = t.n - 1;
@@ -59,19 +80,18 @@ __global__ __launch_bounds__(CT) void grad_sumsq_kernel(ClipTable t, double* __r
         if (t.f32[i]) {
             const float* g = (const float*)t.g[i] + at;
             const int n4 = wide ? n / 4 : 0;
-            for (int k = threadIdx.x; k < n4; k += CT) {
-                const float4 v = ((const float4*)g)[k];
-                s += sq(v.x) + sq(v.y) + sq(v.z) + sq(v.w);
-            }
+            each16(g, n4, [&](int, u32x4_c v) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) s += sq(__uint_as_float(v[e]));
+            });
             for (int k = 4 * n4 + threadIdx.x; k < n; k += CT) s += sq(g[k]);
         } else {
             const uint16_t* g = (const uint16_t*)t.g[i] + at;
             const int n8 = wide ? n / 8 : 0;
-            for (int k = threadIdx.x; k < n8; k += CT) {
-                const uint4 v = ((const uint4*)g)[k];
-                s += sq(bf16_lo(v.x)) + sq(bf16_hi(v.x)) + sq(bf16_lo(v.y)) + sq(bf16_hi(v.y));
-                s += sq(bf16_lo(v.z)) + sq(bf16_hi(v.z)) + sq(bf16_lo(v.w)) + sq(bf16_hi(v.w));
-            }
+            each16(g, n8, [&](int, u32x4_c v) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) s += sq(bf16_lo(v[e])) + sq(bf16_hi(v[e]));
+            });
             for (int k = 8 * n8 + threadIdx.x; k < n; k += CT) s += sq(bf16_lo(g[k]));
         }
     }
@@ -109,7 +129,8 @@ __global__ __launch_bounds__(CT) void grad_scale_kernel(ClipTable t, const doubl
                                                         float max_norm, float* norm, float* coef) {
     const float f = grad_coef(part, parts, max_norm, norm, coef);
     const int chunks = t.first[t.n];
-    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    // backwards: what was summed last may still be cached
+    for (int c = chunks - 1 - blockIdx.x; c >= 0; c -= (int)gridDim.x) {
         const int i = chunk_tensor(t, c);
         if (f == 1.0f && t.out[i] == t.g[i]) continue;  // nothing to clip, in place
         const int64_t at = (int64_t)(c - t.first[i]) * CLIP_CHUNK;
@@ -120,19 +141,23 @@ __global__ __launch_bounds__(CT) void grad_scale_kernel(ClipTable t, const doubl
             const float* g = (const float*)t.g[i] + at;
             float* o = (float*)t.out[i] + at;
             const int n4 = wide ? n / 4 : 0;
-            for (int k = threadIdx.x; k < n4; k += CT) {
-                const float4 v = ((const float4*)g)[k];
-                ((float4*)o)[k] = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-            }
+            each16(g, n4, [&](int k, u32x4_c v) {
+                u32x4_c w;
+#pragma unroll
+                for (int e = 0; e < 4; e++) w[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                __builtin_nontemporal_store(w, (u32x4_c*)o + k);
+            });
             for (int k = 4 * n4 + threadIdx.x; k < n; k += CT) o[k] = g[k] * f;
         } else {
             const uint16_t* g = (const uint16_t*)t.g[i] + at;
             uint16_t* o = (uint16_t*)t.out[i] + at;
             const int n8 = wide ? n / 8 : 0;
-            for (int k = threadIdx.x; k < n8; k += CT) {
-                const uint4 v = ((const uint4*)g)[k];
-                ((uint4*)o)[k] = make_uint4(scale2(v.x, f), scale2(v.y, f), scale2(v.z, f), scale2(v.w, f));
-            }
+            each16(g, n8, [&](int k, u32x4_c v) {
+                u32x4_c w;
+#pragma unroll
+                for (int e = 0; e < 4; e++) w[e] = scale2(v[e], f);
+                __builtin_nontemporal_store(w, (u32x4_c*)o + k);
+            });
             for (int k = 8 * n8 + threadIdx.x; k < n; k += CT) o[k] = (uint16_t)scale2(g[k], f);
         }
     }
