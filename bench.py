@@ -1,7 +1,7 @@
 """Benchmark of the fine-grained FP8 linear on one MI355X.
 
     python bench.py [--gpus 1] [--steps 20] [--warmup 5] [--no-cpu] [--no-workloads] [--accum mfma8|fp32]
-    python bench.py --workload expert_backward|grouped_upproj|decode_grouped|moe_backward
+    python bench.py --workload expert_backward|grouped_upproj|decode_grouped|moe_backward|ffn_step
     python bench.py --traffic-probe     # plain copy of known size, for counter scaling
     python bench.py --library-ceiling   # vendor GEMMs on the dense shape, for context
 
@@ -45,6 +45,12 @@ measured on, each a step of its own kernels with HIP events:
   moe_backward: the up-projection experts' backward pass: dY quantised
     1x128, M-grouped Dgrad on the transposed forward weight codes, dY and X
     quantised in 128x1 groups per expert, K-grouped Wgrad, fp32 out.
+  ffn_step (only by --workload): a gated feed-forward block's training step
+    on 4096 tokens, hidden 7168, inner 18432: the norm before it (quantised
+    1x128), both projections with activation and product (H quantised in the
+    epilogue, pre-activations kept), the down-projection, the norm after it
+    with gate and residual; then the backward pass of all of it, every GEMM in
+    FP8, and the two weight gradients clipped by their global norm.
 --workload NAME prints one such workload as the line instead.
 
 `cpu_baseline` is the CPU oracle on a bounded sub-block of the dense
@@ -69,9 +75,9 @@ PEAK_HBM_GBPS = 8000.0     # MI355X HBM3E
 # per-launch HBM traffic and counters of every workload kernel, written by
 # --summarize-profile from the rocprofv3 passes over --profile-kernels
 PROFILE_SUMMARY = os.path.join(ROOT, "profiles", "kernels_per_launch.md")
-PROFILE_SOURCES = ["block_scaled_gemm_amd/csrc/gemm.hip", "block_scaled_gemm_amd/csrc/quant.hip",
-                   "block_scaled_gemm_amd/csrc/device.h", "block_scaled_gemm_amd/csrc/kernels.h",
-                   "block_scaled_gemm_amd/csrc/api.cpp"]
+PROFILE_SOURCES = ["block_scaled_gemm_amd/csrc/" + f for f in (
+    "gemm.hip", "gemm_tile.h", "quant.hip", "gated.hip", "norm.hip", "clip.hip", "device.h", "kernels.h",
+    "block_kernels.h", "api.cpp", "block_api.cpp")]
 PROFILE_CALLS = 3
 # the dense Fprop GEMM of the default line, as --profile-kernels labels it
 DENSE_GEMM_LABEL = "gemm 4096x18432x7168 (FP32 scales, FP8 matrix cores)"
@@ -505,6 +511,88 @@ def build_moe_backward(d, accum, dev):
     return kernels, 4.0 * rows * Nw * Kw, config
 
 
+def build_ffn_step(accum, dev):
+    """A gated feed-forward block, forward and backward, at the dense Fprop's
+    sizes; x is the residual stream, y0 what the block's forward left in it."""
+    import torch
+    import block_scaled_gemm_amd as bs
+    T, D, F = M, K, N
+    gen = torch.Generator(device=dev).manual_seed(0)
+    rnd = lambda r, c, sd: (torch.randn(r, c, generator=gen, device=dev) * sd).bfloat16()
+    x, dxo, dh = rnd(T, D, 1.0), rnd(T, D, 1e-3), rnd(T, D, 1e-3)
+    one = torch.ones(D, dtype=torch.float32, device=dev)
+    gate = torch.full((1, D), 0.5, dtype=torch.float32, device=dev)
+    qw, sw, qwt = bs.fp8_quant_block(rnd(2 * F, D, 0.02), transpose=True)
+    qwd, swd, qwdt = bs.fp8_quant_block(rnd(D, F, 0.02), transpose=True)
+    o = {}
+
+    def gated():
+        o["qh"], o["sh"], o["gu"] = bs.fp8_gated_gemm_quant(o["pre"].q, o["pre"].s, qw, sw, save_gu=True, accum=accum)
+
+    def norm_pre():
+        o["pre"] = bs.fp8_norm_residual(x, one, want_h=True)
+
+    def down():
+        o["y"] = bs.linear_fprop(o["qh"], o["sh"], qwd, swd, accum=accum)
+
+    def seam():
+        o["seam"] = bs.fp8_norm_residual(x, one, y=o["y"], w_post=one, gate=gate)
+
+    def seam_bwd():
+        o["post"] = bs.fp8_norm_residual_backward(dxo, dh, o["seam"].xo, o["seam"].rstd_x, one, y=o["y"],
+                                                  rstd_y=o["seam"].rstd_y, w_post=one, gate=gate)
+
+    def dual():
+        o["dy"] = bs.fp8_quant_dual(o["post"].dy)
+
+    def dgrad_down():
+        o["dh"] = bs.linear_dgrad(o["dy"][0], o["dy"][1], qwdt, swd, bs.OUT_BF16, accum=accum)
+
+    def gated_bwd():
+        o["g"] = bs.fp8_gated_backward(o["dh"], o["gu"])
+
+    def dgrad():
+        o["dx"] = bs.linear_dgrad(o["g"][0], o["g"][1], qwt, sw, bs.OUT_BF16, accum=accum)
+
+    def cols():
+        o["xt"] = bs.fp8_quant_tile(o["pre"].h, bs.AXIS_COL)
+
+    def wgrad():
+        o["dw"] = bs.linear_wgrad(o["g"][2], o["g"][3], *o["xt"], accum=accum)
+
+    def wgrad_down():
+        o["dwd"] = bs.linear_wgrad(o["dy"][2], o["dy"][3], o["g"][4], o["g"][5], accum=accum)
+
+    def pre_bwd():
+        o["first"] = bs.fp8_norm_residual_backward(o["post"].dx, o["dx"], x, o["pre"].rstd_x, one)
+
+    def clip():
+        bs.fp8_grad_clip([o["dw"], o["dwd"]], 1.0)
+
+    E = T * D
+    s128 = lambda n: n + n / 32  # codes and their fp32 scales per 128
+    weights = 3 * F * D
+    kernels = [
+        (f"norm X[{T}x{D}] -> codes and bf16", norm_pre, 4 * E + s128(E), "GB/s"),
+        (f"gated gemm {T}x{F}x{D} (quantised, pre-activations kept)", gated, 4.0 * T * F * D / 1e3, "TFLOP/s"),
+        (f"down gemm {T}x{D}x{F}", down, 2.0 * T * F * D / 1e3, "TFLOP/s"),
+        (f"norm, gate, residual [{T}x{D}]", seam, 6 * E + s128(E), "GB/s"),
+        (f"norm, gate, residual backward [{T}x{D}]", seam_bwd, 12 * E, "GB/s"),
+        (f"quant_dual dY[{T}x{D}]", dual, 2 * E + 2 * s128(E), "GB/s"),
+        (f"down dgrad {T}x{F}x{D}", dgrad_down, 2.0 * T * F * D / 1e3, "TFLOP/s"),
+        (f"gated backward [{T}x{F}]", gated_bwd, T * F * 6 + 5 * s128(T * F), "GB/s"),
+        (f"gate and up dgrad {T}x{D}x{2 * F}", dgrad, 4.0 * T * F * D / 1e3, "TFLOP/s"),
+        (f"quant_tile COL X[{T}x{D}]", cols, 2 * E + s128(E), "GB/s"),
+        (f"gate and up wgrad {2 * F}x{D}x{T}", wgrad, 4.0 * T * F * D / 1e3, "TFLOP/s"),
+        (f"down wgrad {D}x{F}x{T}", wgrad_down, 2.0 * T * F * D / 1e3, "TFLOP/s"),
+        (f"norm backward [{T}x{D}]", pre_bwd, 8 * E, "GB/s"),
+        ("clip two weight gradients", clip, 12 * weights, "GB/s"),
+    ]
+    config = {"workload": f"ffn_step: gated feed-forward block, {T} tokens, hidden {D}, inner {F}, forward and "
+                          "backward with norms, gate, residual and clipping"}
+    return kernels, 18.0 * T * F * D, config
+
+
 PEAK_UNIT = {"TFLOP/s": (PEAK_FP8_TFLOPS, "mfma"), "GB/s": (PEAK_HBM_GBPS, "hbm")}
 
 
@@ -612,6 +700,8 @@ def profile_kernels():
     del up
     torch.cuda.empty_cache()
     run("decode_grouped", build_grouped("decode_grouped", inputs.decode_grouped(), bs.ACCUM_MFMA8, dev)[0])
+    torch.cuda.empty_cache()
+    run("ffn_step", build_ffn_step(bs.ACCUM_MFMA8, dev)[0])
     print(json.dumps({"profile_manifest": manifest, "source_hash": source_hash(PROFILE_SOURCES)}), flush=True)
 
 
@@ -769,6 +859,8 @@ def other_workload(name, args, data=None):
     accum = {"fp32": bs.ACCUM_FP32, "mfma8": bs.ACCUM_MFMA8, "mfma8_pow2": bs.ACCUM_MFMA8_POW2}[accum_name]
     if name == "expert_backward":
         built = build_expert_backward(data or inputs.expert_backward(), accum, dev)
+    elif name == "ffn_step":
+        built = build_ffn_step(accum, dev)
     elif name == "moe_backward":
         built = build_moe_backward(data or inputs.grouped_upproj(), accum, dev)
     else:
@@ -804,7 +896,8 @@ def main():
     ap.add_argument("--library-ceiling", action="store_true",
                     help="time the vendor GEMMs on the dense shape (context only)")
     ap.add_argument("--workload", default="dense_fprop",
-                    choices=["dense_fprop", "expert_backward", "grouped_upproj", "decode_grouped", "moe_backward"])
+                    choices=["dense_fprop", "expert_backward", "grouped_upproj", "decode_grouped", "moe_backward",
+                             "ffn_step"])
     args = ap.parse_args()
     if args.gpus != 1 or int(os.environ.get("WORLD_SIZE", "1")) > 1:
         print("bench.py measures one GPU only: the fine-grained FP8 linear here is a "
@@ -837,7 +930,7 @@ def main():
         line = {"metric": METRIC, "value": rep["value"], "unit": "TFLOP/s", "n_gpus": 1, "steps": args.steps,
                 "warmup": args.warmup, "ms_per_step": rep["ms_per_step"], "higher_is_better": True,
                 "scaling": "weak", "vs_baseline": None, "dtype": "fp8_e4m3",
-                "data": "synthetic (seeded numpy, shapes and distributions of the workload)",
+                "data": "synthetic (seeded, shapes and distributions of the workload)",
                 "config": rep["config"], "settle": rep["settle"], "roofline": rep["roofline"],
                 "kernels": rep["kernels"], "cpu_baseline": None}
         print(json.dumps(line), flush=True)

@@ -26,6 +26,7 @@ and the feed-forward block around them (block.py):
     fp8_grouped_gated_backward(offsets, dh, gu, ...)          -> the same
     fp8_norm_residual(x, w_pre, y, w_post, gate, ...)         -> (xo, h, q, s, rstd_y, rstd_x)
     fp8_norm_residual_backward(dxo, dh, xo, rstd_x, w_pre, ...) -> (dx, dy, dw_pre, dw_post, dgate)
+    gated_ffn_fprop(qx, sx, qw, sw, qwd, swd, act) -> (y, gu) and gated_ffn_backward(...): the layer's GEMMs
     fp8_grad_norm(grads) -> norm;  fp8_grad_clip(grads, max_norm, out=None) -> (norm, coef)
 
 bf16 inputs are ``torch.bfloat16`` tensors (their bit patterns are what the
@@ -467,4 +468,4 @@ from . import block  # noqa: E402  (needs the names above)
 from .block import (ACT_GELU, ACT_SILU, NormResidual, NormResidualGrads, fp8_gated_backward,  # noqa: E402,F401
                     fp8_gated_gemm, fp8_gated_gemm_quant, fp8_grad_clip, fp8_grad_norm, fp8_grouped_gated_backward,
                     fp8_grouped_gated_gemm, fp8_grouped_gated_gemm_quant, fp8_norm_residual,
-                    fp8_norm_residual_backward, gated_workspace_bytes)
+                    fp8_norm_residual_backward, gated_ffn_backward, gated_ffn_fprop, gated_workspace_bytes, quant_cols)

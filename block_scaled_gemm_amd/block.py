@@ -11,8 +11,9 @@ import ctypes
 
 import torch
 
-from . import (ACCUM_FP32, ACCUM_MFMA8_POW2, OUT_BF16, OUT_F32, SCALE_FP32, _check, _check_pow2_mode, _ptr,
-               grouped_col_bound, lib)
+from . import (ACCUM_FP32, ACCUM_MFMA8_POW2, AXIS_COL, AXIS_ROW, OUT_BF16, OUT_F32, SCALE_FP32, _check,
+               _check_pow2_mode, _ptr, fp8_quant_tile, fp8_quant_tile_grouped_col, grouped_col_bound, lib,
+               linear_dgrad, linear_fprop, linear_wgrad)
 
 ACT_SILU, ACT_GELU = 0, 1
 
@@ -290,6 +291,43 @@ def fp8_grouped_gated_backward(offsets, dh, gu, act=ACT_SILU, scale_mode=SCALE_F
                            scale_mode, (qr, sr), (qc, sc), (qh, sh), (with_rows, with_cols, with_h))
 
 
+# ---- the gated layer's GEMMs -----------------------------------------------------------
+
+def quant_cols(x, scale_mode=SCALE_FP32):
+    """bf16 x [M, C] in 128x1 groups for a Wgrad, any M: codes [C, P] and
+    scales [P/128, C], P = M rounded up to 128, zero codes past row M."""
+    M, C = _matrix(x, "x")
+    if M % 128 == 0:
+        return fp8_quant_tile(x, AXIS_COL, scale_mode)
+    P = (M + 127) // 128 * 128
+    offsets = torch.arange(0, M + 1, M, dtype=I32, device=x.device)  # one range: 0, M
+    q, s = fp8_quant_tile_grouped_col(x, offsets, scale_mode)
+    return q[:, :P], s[:P // 128]
+
+
+def gated_ffn_fprop(qx, sx, qw, sw, qwd, swd, act=ACT_SILU, out_dtype=OUT_BF16, scale_mode=SCALE_FP32,
+                    accum=ACCUM_FP32, save_gu=True):
+    """Y = (act(X Wg^T) * (X Wu^T)) Wd^T from quant_tile(X, ROW) and the block
+    quantisations of the stacked gate and up weights [2N, K] and of Wd [D, N].
+    H leaves the first kernel in FP8.  Returns (y [M, D], gu or None)."""
+    qh, sh, gu = fp8_gated_gemm_quant(qx, sx, qw, sw, act, scale_mode, save_gu=save_gu, accum=accum)
+    return linear_fprop(qh, sh, qwd, swd, out_dtype, accum=accum), gu
+
+
+def gated_ffn_backward(dy, gu, qxt, sxt, qwt, sw, qwdt, swd, act=ACT_SILU, scale_mode=SCALE_FP32, out_dtype=OUT_BF16,
+                       accum=ACCUM_FP32):
+    """Backward of gated_ffn_fprop from dY [M, D] and gu (bf16): qxt, sxt =
+    quant_cols(X); qwt, qwdt the transposed codes of the two weights
+    (fp8_quant_block(transpose=True)) with their scales.  Returns (dx [M, K]
+    as out_dtype, dw [2N, K], dwd [D, N], both fp32)."""
+    qdy, sdy = fp8_quant_tile(dy, AXIS_ROW, scale_mode)
+    qdyt, sdyt = quant_cols(dy, scale_mode)
+    dh = linear_dgrad(qdy, sdy, qwdt, swd, OUT_BF16, accum=accum)
+    qr, sr, qc, sc, qh, sh = fp8_gated_backward(dh, gu, act, scale_mode)
+    return (linear_dgrad(qr, sr, qwt, sw, out_dtype, accum=accum),
+            linear_wgrad(qc, sc, qxt, sxt, accum=accum), linear_wgrad(qdyt, sdyt, qh, sh, accum=accum))
+
+
 # ---- norms ---------------------------------------------------------------------------
 
 NormResidual = collections.namedtuple("NormResidual", "xo h q s rstd_y rstd_x")
@@ -327,11 +365,13 @@ def fp8_norm_residual(x, w_pre=None, y=None, w_post=None, gate=None, gate_rows=N
     if y is not None:
         xo, xop, ldxo = _out(xo, "xo", BF16, dev, (M, D), x)
     # the statistics in one allocation
-    stats = torch.empty((2, M), dtype=F32, device=x.device)
-    ry, rx = stats[0] if w_post is not None else None, None
-    if w_pre is not None:
+    ry, rx = torch.empty((2, M), dtype=F32, device=x.device).unbind()
+    if w_post is None:
+        ry = None
+    if w_pre is None:
+        rx = None
+    else:
         prep = _arg(w_pre, "w_pre", F32, dev, (D,))[0]
-        rx = stats[1]
         if quantise or q is not None:
             q, s, out = _quant_out(q, s, M, D, dev, x)
         if want_h or h is not None:
@@ -364,8 +404,11 @@ def fp8_norm_residual_backward(dxo, dh, xo, rstd_x, w_pre, y=None, rstd_y=None, 
     dyp, lddy = None, 0
     if y is not None:
         dy, dyp, lddy = _out(dy, "dy", BF16, dev, (M, D), lead)
-    dw = torch.empty((2, D), dtype=F32, device=lead.device)
-    dw_pre, dw_post = dw[0] if dh is not None else None, dw[1] if w_post is not None else None
+    dw_pre, dw_post = torch.empty((2, D), dtype=F32, device=lead.device).unbind()
+    if dh is None:
+        dw_pre = None
+    if w_post is None:
+        dw_post = None
     dgate = torch.empty_like(gate) if gate is not None else None
     ws = _workspace(workspace, lib().fp8_norm_backward_workspace_bytes(M, D), dev, lead)
     _check(lib().fp8_norm_residual_backward(M, D, dxop, lddxo, dhp, lddh, xop, ldxo, rxp, prep, yp, ldy, ryp, wp, gp,

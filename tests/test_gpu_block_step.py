@@ -1,0 +1,230 @@
+"""The feed-forward block's operators run together as a training step uses
+them: norm, gated layer, norm after the block with gate and residual, the
+whole backward pass, and clipping.  Every stage is checked against its 64-bit
+form on the values that the stage was given, so quantisation of one stage does
+not blur the next."""
+import pytest
+import torch
+
+import block_ref as ref
+import block_scaled_gemm_amd as bs
+from block_ref import F64, U32, UBF16
+
+pytestmark = pytest.mark.gpu
+
+
+def up(t):
+    return t.detach().cpu().to(F64)
+
+
+def near(got, want, err, unit, tag):
+    off = (up(got) - want).abs()
+    worst = float((off / (err + unit * (want.abs() + err) + 1e-30)).max())
+    assert worst <= 1.0, (tag, worst)
+
+
+def gemm_err(a, b, accum):
+    """Error of an FP8 GEMM of a [M, K] and b [N, K]: fp32 sums, and the FP8
+    matrix cores' 2^-10 of the summed magnitudes."""
+    rel = (160 + a.shape[1] // 128) * U32 + (2.0 ** -10 if accum != bs.ACCUM_FP32 else 0.0)
+    return rel * (a.abs() @ b.abs().t())
+
+
+def cols(q, s, rows):
+    return ref.cols64(q, s)[:rows]
+
+
+@pytest.mark.parametrize("accum", [bs.ACCUM_FP32, bs.ACCUM_MFMA8])
+@pytest.mark.parametrize("M", [256, 200, 1])
+def test_dense_training_step(hip, M, accum):
+    D, N, act, alpha = 256, 384, bs.ACT_SILU, 0.75
+    gen = torch.Generator().manual_seed(M)
+    rnd = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    dev = lambda t: t.cuda()  # noqa: E731
+    x0, y0, dxo, dh2 = (dev(rnd(M, D).bfloat16()) for _ in range(4))
+    w1, w2, wpost, gate = (dev(1 + 0.2 * rnd(D)) for _ in range(4))
+    gate = gate.view(1, D)
+    W, Wd = dev((rnd(2 * N, D) * 0.06).bfloat16()), dev((rnd(D, N) * 0.06).bfloat16())
+    qw, sw, qwt = bs.fp8_quant_block(W, transpose=True)
+    qwd, swd, qwdt = bs.fp8_quant_block(Wd, transpose=True)
+
+    # forward: the norm before, the layer, the norm after with gate and residual
+    pre = bs.fp8_norm_residual(x0, w1, want_h=True)
+    y, gu = bs.gated_ffn_fprop(pre.q, pre.s, qw, sw, qwd, swd, act, accum=accum)
+    seam = bs.fp8_norm_residual(x0, w2, y=y, w_post=wpost, gate=gate, alpha=alpha, want_h=True)
+    # backward
+    post = bs.fp8_norm_residual_backward(dxo, dh2, seam.xo, seam.rstd_x, w2, y=y, rstd_y=seam.rstd_y, w_post=wpost,
+                                         gate=gate, alpha=alpha)
+    qxt, sxt = bs.quant_cols(pre.h)
+    dx1, dw, dwd = bs.gated_ffn_backward(post.dy, gu, qxt, sxt, qwt, sw, qwdt, swd, act, accum=accum)
+    first = bs.fp8_norm_residual_backward(post.dx, dx1, x0, pre.rstd_x, w1)
+    grads = [dw, dwd, first.dw_pre, post.dw_pre, post.dw_post, post.dgate]
+    total, coef = bs.fp8_grad_clip(grads, 1.0, out=[torch.empty_like(g) for g in grads])
+    torch.cuda.synchronize()
+
+    # the layer, from the codes it was given
+    X, Wq, Wdq = ref.rows64(pre.q, pre.s), ref.blocks64(qw, sw), ref.blocks64(qwd, swd)
+    H, G, U, sg, su = ref.gated(X, Wq, act)
+    rel = (160 + D // 128) * U32 + (2.0 ** -10 if accum != bs.ACCUM_FP32 else 0.0)
+    near(gu[:, :N], G, rel * sg, UBF16, "G")
+    near(gu[:, N:], U, rel * su, UBF16, "U")
+    # H went through 1x128 codes: each of its values is off by 2^-4, or the
+    # subnormal step 2^-10 of the group's scale (amax / 448)
+    eh = 1.13 * rel * sg * (U.abs() + rel * su) + ref.act(G, act).abs() * rel * su + 64 * U32 * H.abs()
+    amax = (H.abs() + eh).view(M, N // 128, 128).amax(2).repeat_interleave(128, 1)
+    qerr = eh + ref.UE4M3 * 1.001 * (H.abs() + eh) + 2.0 ** -10 * amax / 448 * 1.001
+    near(y, H @ Wdq.t(), qerr @ Wdq.abs().t() + gemm_err(H.abs() + qerr, Wdq, accum), UBF16, "y")
+
+    # backward GEMMs, from dy's codes
+    qdy, sdy = bs.fp8_quant_tile(post.dy)
+    dY = ref.rows64(qdy, sdy)
+    dh = bs.linear_dgrad(qdy, sdy, qwdt, swd, bs.OUT_BF16, accum=accum)
+    near(dh, dY @ Wdq, gemm_err(dY, Wdq.t().contiguous(), accum), UBF16, "dh")
+    qr, sr, qc, sc, qh, sh = bs.fp8_gated_backward(dh, gu, act)
+    near(dx1, ref.rows64(qr, sr) @ Wq, gemm_err(ref.rows64(qr, sr), Wq.t().contiguous(), accum), UBF16, "dx")
+    dG, Xc = ref.cols64(qc, sc).t().contiguous(), ref.cols64(qxt, sxt).t().contiguous()
+    near(dw, dG @ Xc.t(), gemm_err(dG, Xc, accum), U32, "dW")
+    qdt, sdt = bs.quant_cols(post.dy)
+    dYc, Hc = ref.cols64(qdt, sdt).t().contiguous(), ref.cols64(qh, sh).t().contiguous()
+    near(dwd, dYc @ Hc.t(), gemm_err(dYc, Hc, accum), U32, "dWd")
+    assert bool((dG[:, M:] == 0).all()) and bool((Hc[:, M:] == 0).all()), "padding adds nothing"
+    # both groupings and H stand for the same gradients
+    want = torch.cat(ref.gated_backward(up(dh), up(gu[:, :N]), up(gu[:, N:]), act)[:2], 1)
+    for got in (ref.rows64(qr, sr), dG.t()[:M]):
+        assert float((got - want).norm() / want.norm()) < ref.UE4M3
+    # the clipped gradients
+    norm = torch.stack([up(g).norm() for g in grads]).norm()
+    assert abs(float(total) - float(norm)) <= 4 * U32 * float(norm)
+    assert abs(float(coef) - min(1.0, 1.0 / (float(norm) + 1e-6))) <= 4 * U32
+
+
+def test_experts_training_step(hip):
+    """Experts: grouped gated product, grouped backward, and the K-grouped and
+    M-grouped GEMMs that read its outputs."""
+    sizes, D, N, act = [70, 0, 129, 1], 256, 128, bs.ACT_GELU
+    G, M = len(sizes), sum(sizes)
+    gen = torch.Generator().manual_seed(1)
+    off = torch.tensor([0, 70, 70, 199, 200], dtype=torch.int32, device="cuda")
+    x = torch.randn(M, D, generator=gen).bfloat16().cuda()
+    dh = torch.randn(M, N, generator=gen).bfloat16().cuda()
+    W = (torch.randn(G * 2 * N, D, generator=gen) * 0.06).bfloat16().cuda()
+    qx, sx = bs.fp8_quant_tile(x)
+    qw, sw, qwt = bs.fp8_quant_block(W, transpose=True)
+    acc = bs.ACCUM_FP32
+    h, gu = bs.fp8_grouped_gated_gemm(off, qx, sx, qw.view(G, 2 * N, D), sw.view(G, 2 * N // 128, D // 128), act,
+                                      save_gu=True, accum=acc)
+    qr, sr, qc, sc, qh, sh = bs.fp8_grouped_gated_backward(off, dh, gu, act)
+    dx = bs.moe_dgrad(off, qr, sr, qwt, sw, G, accum=acc)
+    qxt, sxt = bs.fp8_quant_tile_grouped_col(x, off)
+    dw = bs.fp8_grouped_gemm_kgrouped(off, qc, sc, qxt, sxt, accum=acc)
+    hh = bs.fp8_grouped_gemm_kgrouped(off, qh, sh, qxt, sxt, accum=acc)
+    Wq, dR = ref.blocks64(qw, sw), ref.rows64(qr, sr)
+    row = p = 0
+    for e, n in enumerate(sizes):
+        w = Wq[e * 2 * N:(e + 1) * 2 * N]
+        P = (n + 127) // 128 * 128
+        if n:
+            near(dx[row:row + n], dR[row:row + n] @ w, gemm_err(dR[row:row + n], w.t().contiguous(), acc), U32, "dx")
+        # (with no padded rows the sums are empty: zeros)
+        part = lambda q, s: ref.cols64(q[:, p:p + P], s[p // 128:(p + P) // 128]).t().contiguous()  # noqa: E731
+        a, b, c = part(qc, sc), part(qxt, sxt), part(qh, sh)
+        near(dw[e], a @ b.t(), gemm_err(a, b, acc) + 1e-30, U32, f"dW of expert {e}")
+        near(hh[e], c @ b.t(), gemm_err(c, b, acc) + 1e-30, U32, f"H X of expert {e}")
+        if not n:
+            assert bool((dw[e] == 0).all())
+        row, p = row + n, p + P
+
+
+def test_offsets_past_32_bits(hip):
+    """Matrices whose byte and element offsets pass 2^32: the last rows come out
+    as those of a small matrix."""
+    D = 8192
+    M = (1 << 31) // D + 40
+    x = torch.ones(1, D, dtype=torch.bfloat16, device="cuda").repeat(M, 1)
+    gen = torch.Generator().manual_seed(2)
+    tail = torch.randn(3, D, generator=gen).bfloat16().cuda()
+    x[-3:] = tail
+    w = torch.ones(D, device="cuda")
+    r = bs.fp8_norm_residual(x, w, y=x, w_post=w)
+    t = bs.fp8_norm_residual(tail, w, y=tail, w_post=w)
+    assert torch.equal(r.xo[-3:], t.xo) and torch.equal(r.q[-3:], t.q) and torch.equal(r.s[:, -3:], t.s)
+    g = bs.fp8_norm_residual_backward(x, None, None, None, None, y=x, rstd_y=r.rstd_y, w_post=w)
+    gt = bs.fp8_norm_residual_backward(tail, None, None, None, None, y=tail, rstd_y=t.rstd_y, w_post=w)
+    assert torch.equal(g.dx[-3:], gt.dx) and torch.equal(g.dy[-3:], gt.dy)
+    del r, g
+    dh, gu = x[:, :D // 2], x  # dh rows D apart
+    qr, sr, _, _, qh, sh = bs.fp8_gated_backward(dh, gu, with_cols=False)
+    n = 128 + M % 128
+    qt, st, _, _, ht, sht = bs.fp8_gated_backward(dh[-n:].contiguous(), gu[-n:].contiguous(), with_cols=False)
+    assert torch.equal(qr[-n:], qt) and torch.equal(sr[:, -n:], st)
+    P = (n + 127) // 128 * 128
+    assert torch.equal(qh[:, -P:], ht) and torch.equal(sh[-P // 128:], sht)
+    norm = bs.fp8_grad_norm([x])
+    want = (float(M - 3) * D + float(tail.double().square().sum())) ** 0.5
+    assert abs(float(norm) - want) <= 2 * U32 * want
+
+
+def test_binding_refusals(hip):
+    """Wrong types, shapes and layouts are refused before the library is called."""
+    u8 = torch.zeros(4, 256, dtype=torch.uint8, device="cuda")
+    sa, w, sw = torch.ones(2, 4, device="cuda"), torch.zeros(256, 256, dtype=torch.uint8, device="cuda"), \
+        torch.ones(2, 2, device="cuda")
+    ok = (u8, sa, w, sw)
+    bs.fp8_gated_gemm(*ok)
+    bad = [(u8.float(), sa, w, sw), (u8, sa.double(), w, sw), (u8, sa[:1], w, sw), (u8, sa[:, :3], w, sw),
+           (u8, sa, w[:, :128], sw), (u8, sa, w, sw[:1]), (u8, sa, w.cpu(), sw), (u8.t(), sa, w, sw),
+           (u8, sa, w.t(), sw), (u8[0], sa, w, sw)]
+    for args in bad:
+        with pytest.raises((TypeError, ValueError)):
+            bs.fp8_gated_gemm(*args)
+    for kw in (dict(d=torch.empty(3, 128, dtype=torch.bfloat16, device="cuda")),
+               dict(d=torch.empty(4, 128, device="cuda")),
+               dict(gu=torch.empty(4, 128, dtype=torch.bfloat16, device="cuda"))):
+        with pytest.raises((TypeError, ValueError)):
+            bs.fp8_gated_gemm(*ok, **kw)
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    bs.fp8_grouped_gated_gemm(off, u8, sa, w[None], sw[None])
+    for args in ((off.long(), u8, sa, w[None], sw[None]), (off[:1], u8, sa, w[None], sw[None]),
+                 (off, u8, sa, w, sw), (off, u8, sa, w[None], sw)):
+        with pytest.raises((TypeError, ValueError)):
+            bs.fp8_grouped_gated_gemm(*args)
+    with pytest.raises(ValueError):
+        bs.fp8_grouped_gated_gemm(off, u8, sa, w[None], sw[None], rows_bound=5)
+    b = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    v = torch.ones(256, device="cuda")
+    for f in (lambda: bs.fp8_norm_residual(b, v[:128]), lambda: bs.fp8_norm_residual(b, v, y=b[:3]),
+              lambda: bs.fp8_norm_residual(b.float(), v),
+              lambda: bs.fp8_norm_residual(b, v, y=b, gate=torch.ones(1, 256, device="cuda"), gate_rows=2),
+              lambda: bs.fp8_norm_residual(b, v, y=b, gate=torch.ones(1, 256, device="cuda"), gate_rows=0),
+              lambda: bs.fp8_norm_residual_backward(None, b, b, v, v),
+              lambda: bs.fp8_gated_backward(b, b), lambda: bs.fp8_gated_backward(b[:, :128], b.float()),
+              lambda: bs.fp8_grad_norm([v.half()]), lambda: bs.fp8_grad_norm([b.t()]),
+              lambda: bs.fp8_grad_clip([v], 1.0, out=[v[:5]]), lambda: bs.fp8_grad_clip([v, v], 1.0, out=[v])):
+        with pytest.raises((TypeError, ValueError)):
+            f()
+    with pytest.raises(bs.FP8BSError):
+        bs.fp8_norm_residual(b, None)  # neither a residual sum nor a norm
+    with pytest.raises(bs.FP8BSError):
+        bs.fp8_norm_residual(b, v, w_post=v)  # a norm of no y
+    torch.cuda.synchronize()
+
+
+def test_two_streams_at_once(hip):
+    """Calls on two streams, each with its own outputs and workspace, at the same time."""
+    M, N, K = 40, 128, 4096
+    gen = torch.Generator().manual_seed(7)
+    x = torch.randn(M, K, generator=gen).bfloat16().cuda()
+    qx, sx = bs.fp8_quant_tile(x)
+    qw, sw, _ = bs.fp8_quant_block((torch.randn(2 * N, K, generator=gen) * 0.05).bfloat16().cuda())
+    y = torch.randn(3000, 512, generator=gen).bfloat16().cuda()
+    w = torch.ones(512, device="cuda")
+    want, _ = bs.fp8_gated_gemm(qx, sx, qw, sw)
+    wantn = bs.fp8_norm_residual(y, w, y=y, w_post=w)
+    torch.cuda.synchronize()
+    got, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append((bs.fp8_gated_gemm(qx, sx, qw, sw)[0], bs.fp8_norm_residual(y, w, y=y, w_post=w)))
+    torch.cuda.synchronize()
+    for h, n in got:
+        assert torch.equal(h, want) and torch.equal(n.xo, wantn.xo) and torch.equal(n.q, wantn.q)
