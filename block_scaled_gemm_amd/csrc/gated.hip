@@ -701,11 +701,11 @@ __global__ __launch_bounds__(THREADS) void gated_kernel(GatedArgs p, int64_t til
 // there can be (one more per expert than the rows fill) and the workgroups
 // past the last tile leave.  A workgroup to each row tile, and not to each
 // expert's rows, evens out experts of uneven size (32 experts, 4096 rows: 322
-// us with a workgroup walking its expert's rows).
-template <int ACC>
+// -> 239 us).
+template <int ACC, int TILE>
 __global__ __launch_bounds__(THREADS) void gated_grouped_kernel(GatedArgs p, int64_t tiles_n) {
-    constexpr int TILE = Shape<ACC == 0 ? 21 : 20>::BM;
-    constexpr int BYTES = ACC == 0 ? Lds<21>::BYTES : Lds<21>::BYTES > Lds<20>::BYTES ? Lds<21>::BYTES : Lds<20>::BYTES;
+    static_assert(TILE == Shape<21>::BM || (ACC != 0 && TILE == Shape<20>::BM), "the tallest row tile");
+    constexpr int BYTES = TILE == 128 ? Lds<21>::BYTES : Lds<21>::BYTES > Lds<20>::BYTES ? Lds<21>::BYTES : Lds<20>::BYTES;
     static_assert(Lds<22>::BYTES <= BYTES, "every row-tile shape fits");
     __shared__ __attribute__((aligned(16))) uint8_t smem[BYTES];
     const int64_t total = count_tiles<TILE>(p.offsets, p.G) * tiles_n;
@@ -725,10 +725,10 @@ __global__ __launch_bounds__(THREADS) void gated_grouped_kernel(GatedArgs p, int
     } else {
         if (f.rows <= Shape<22>::BM)
             gated_tile<ACC, 22>(p, T, 0, groups, 0, smem);
-        else if (f.rows <= Shape<21>::BM)
+        else if (TILE == 128 || f.rows <= Shape<21>::BM)
             gated_tile<ACC, 21>(p, T, 0, groups, 0, smem);
         else
-            gated_tile<ACC, 20>(p, T, 0, groups, 0, smem);
+            gated_tile<ACC, TILE == 128 ? 21 : 20>(p, T, 0, groups, 0, smem);
     }
 }
 
@@ -891,10 +891,22 @@ __global__ __launch_bounds__(256) void gated_few_quant_kernel(GatedArgs p) {
 int gated_splits(int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = ((M + 127) / 128) * (N / 128), groups = K / 128;
     if (few_rows(M, N)) return 1;
-    if (tiles == 0 || groups < 16 || tiles >= 128) return 1;
+    if (tiles == 0 || groups < 16 || tiles > 128) return 1;
     int64_t s = 256 / tiles;
     if (s > groups / 8) s = groups / 8;
     return s < 2 ? 1 : (int)s;
+}
+
+// Whether 256-row tiles take less time than 128-row ones, by their rounds of
+// workgroups (one fills a CU's LDS).  A round of 128-row tiles takes about two
+// thirds of the other's time (K = 7168: 62 us against 100; 60 against 85 with
+// power-of-two scales, whose tall tile promotes nothing).  300 x 8192 on 128-row tiles
+// 99 -> 60 us, 2000 x 2048 94 -> 64; 200 x 18432 127 us on them against 107.
+static bool tall_tiles(int64_t tall, int64_t low, int accum) {
+    const int64_t cus = device_cus();
+    tall = (tall + cus - 1) / cus;
+    low = (low + cus - 1) / cus;
+    return (double)tall <= (accum == 2 ? 0.7 : 0.66) * (double)low;
 }
 
 size_t gated_workspace(int64_t M, int64_t N, int64_t K, bool quant) {
@@ -924,7 +936,7 @@ static void launch_gated_acc(const GatedArgs& g, hipStream_t st) {
     } else {
         if (g.M <= Shape<22>::BM)
             launch_gated_shape<ACC, 22>(g, st);
-        else if (g.M <= Shape<21>::BM || g.splits > 1)
+        else if (g.splits > 1 || !tall_tiles((g.M + 255) / 256 * (g.N / 128), (g.M + 127) / 128 * (g.N / 128), ACC))
             launch_gated_shape<ACC, 21>(g, st);
         else
             launch_gated_shape<ACC, 20>(g, st);
@@ -951,21 +963,39 @@ hipError_t launch_gated(const GatedArgs& g, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <int ACC, int TILE>
+static void launch_grouped_tile(const GatedArgs& g, hipStream_t st) {
+    // the rows fill at most this many tiles, and a last tile for each expert
+    int64_t most = (g.M + TILE - 1) / TILE + g.G;
+    if (most > g.M) most = g.M;
+    const int64_t tiles_n = g.N / 128;
+    hipLaunchKernelGGL((gated_grouped_kernel<ACC, TILE>), dim3((unsigned)(tiles_n * most)), dim3(THREADS), 0, st, g,
+                       tiles_n);
+}
+
+template <int ACC>
+static void launch_grouped_acc(const GatedArgs& g, hipStream_t st) {
+    // how the rows fall to the experts is not known here: half a tile over for
+    // each.  1 expert, 3000 rows of 2 x 2048 x 7168: 134 us on 128-row tiles, 105
+    // on 256-row ones; 8 experts, 1000 rows 72 and 95.
+    if constexpr (ACC != 0) {
+        const int64_t tn = g.N / 128;
+        if (tall_tiles((g.M + 128 * g.G) * tn / 256, (g.M + 64 * g.G) * tn / 128, ACC)) {
+            launch_grouped_tile<ACC, 256>(g, st);
+            return;
+        }
+    }
+    launch_grouped_tile<ACC, 128>(g, st);
+}
+
 hipError_t launch_grouped_gated(const GatedArgs& g, hipStream_t st) {
     if (g.G == 0 || g.N == 0) return hipSuccess;
-    const int64_t tiles_n = g.N / 128;
-    const int64_t tile = g.accum == 0 ? Shape<21>::BM : Shape<20>::BM;
-    // the rows fill at most this many tiles, no expert more than its own, and a
-    // last tile each
-    int64_t most = (g.M + tile - 1) / tile + g.G;
-    if (most > g.M) most = g.M;
-    const dim3 grid((unsigned)(tiles_n * most));
     if (g.accum == 0)
-        hipLaunchKernelGGL(gated_grouped_kernel<0>, grid, dim3(THREADS), 0, st, g, tiles_n);
+        launch_grouped_acc<0>(g, st);
     else if (g.accum == 1)
-        hipLaunchKernelGGL(gated_grouped_kernel<1>, grid, dim3(THREADS), 0, st, g, tiles_n);
+        launch_grouped_acc<1>(g, st);
     else
-        hipLaunchKernelGGL(gated_grouped_kernel<2>, grid, dim3(THREADS), 0, st, g, tiles_n);
+        launch_grouped_acc<2>(g, st);
     return hipGetLastError();
 }
 

@@ -647,7 +647,7 @@ static void launch_shape(const GemmArgs& g, hipStream_t st) {
 
 // Compute units of the current device (one workgroup of either shape fills
 // a CU's LDS, so this is also the number of tiles in flight).
-static int device_cus() {
+int device_cus() {
     static int cache[64] = {};
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;

@@ -81,6 +81,9 @@ size_t gemm_workspace(int64_t M, int64_t N, int64_t K);
 // receives the split's cost in rounds of 256 x 256 tiles.
 int64_t wide_columns(int64_t M, int64_t N, int cus, double* cost_out = nullptr);
 
+// Compute units of the current device (256 where it does not say).
+int device_cus();
+
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t st);
 hipError_t launch_grouped_gemm(const GemmArgs& g, hipStream_t st);
 // K-grouped: expert e sums the K groups of its tokens on the padded token

@@ -58,6 +58,8 @@ CASES = [
     (1, 128, 128), (1, 256, 2048), (3, 384, 256), (15, 128, 4352), (16, 256, 640), (8, 18432, 256), (7, 18432, 128), (17, 128, 1152), (32, 256, 4096),
     (33, 128, 3200), (63, 128, 384), (64, 256, 512), (65, 128, 640), (127, 128, 2304),
     (128, 256, 2048), (129, 128, 256), (255, 384, 128), (257, 256, 384), (300, 1408, 512), (513, 128, 1024),
+    # enough columns for the 256-row tiles
+    (200, 18432, 384), (259, 16384, 128),
 ]
 
 
