@@ -37,7 +37,10 @@ __device__ __forceinline__ float gate_sigmoid(const int act, float g, float& dp)
     const float t = -p * l2e;
     const float r = __builtin_fmaf(-p, l2e, -t) - p * rest;
     const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(r, 0.693147181f, 1.0f);
-    return __builtin_amdgcn_rcpf(1.0f + e);
+    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    // GELU is defined by 1 + tanh(z), which is 2 s and in fp32 reaches zero
+    // below 2^-25: taken as zero there (g < -5.17), as the tanh form gives it
+    return act != 0 && s < 0x1p-26f ? 0.0f : s;
 }
 
 __device__ __forceinline__ float gated(int act, float g, float u) {

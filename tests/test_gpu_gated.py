@@ -41,8 +41,9 @@ def bounds(g, u, sg, su, K, accum, act):
     eg, eu = rel * sg, rel * su
     a = ref.act(g, act)
     p = g.abs().clamp_max(20) if act == ref.SILU else 1.6 * (g.abs() + 0.045 * g.abs() ** 3).clamp_max(400)
-    # sigmoid's relative error, p 2^-23 + a few, falls on act(g)
-    eh = 1.13 * eg * (u.abs() + eu) + a.abs() * eu + (a * u).abs() * (8 + 2 * p) * U32
+    # sigmoid's relative error, p 2^-23 + a few, falls on act(g); below 2^-26 GELU's is zero
+    tail = (g * u).abs() * 2.0 ** -26 if act == ref.GELU else 0.0
+    eh = 1.13 * eg * (u.abs() + eu) + a.abs() * eu + (a * u).abs() * (8 + 2 * p) * U32 + tail
     return eg, eu, eh + 1e-30
 
 
@@ -243,7 +244,10 @@ def bwd_bounds(dh, g, u, act):
     a = ref.act(g, act)
     s = torch.where(g == 0, torch.full_like(g, 0.5), a / g)
     terms = s + a.abs() * (1 - s + unit) * dp + a.abs() * dp
-    return (dh * u).abs() * unit * terms + 1e-37, (dh * a).abs() * unit + 1e-37, (a * u).abs() * unit + 1e-37
+    # GELU's sigmoid is zero below 2^-26
+    t = torch.where(s < 2.0 ** -25, torch.full_like(g, 2.0 ** -26), torch.zeros_like(g)) * float(act == ref.GELU)
+    return ((dh * u).abs() * (unit * terms + t * (1 + g.abs() * dp)) + 1e-37, (dh * a).abs() * unit +
+            (dh * g).abs() * t + 1e-37, (a * u).abs() * unit + (g * u).abs() * t + 1e-37)
 
 
 def check_cols(q, s, x, err, pow2, tag):
@@ -276,6 +280,20 @@ def test_backward_dense(hip, M, N, act, pow2):
     assert torch.equal(r[0], qr) and torch.equal(r[1], sr) and r[2] is r[3] is r[4] is r[5] is None
     r = bs.fp8_gated_backward(dh.cuda(), gu.cuda(), act, mode, with_rows=False)
     assert r[0] is None and torch.equal(r[2], qc) and torch.equal(r[4], qh) and torch.equal(r[3], sc)
+
+
+def test_backward_gelu_tail(hip):
+    """One-row groups scale every value to the top of the range, so the tail's
+    zeros show: g <= -5.1875 gives zero H, dG and dU, g >= -5.15625 does not."""
+    N = 128
+    g = -(torch.arange(N) + 40).float() / 16  # -2.5 .. -10.4375
+    g[0], g[1] = -5.15625, -5.1875
+    gu = torch.cat([g, torch.ones(N)]).bfloat16().view(1, 2 * N).cuda()
+    dh = torch.ones(1, N, dtype=torch.bfloat16, device="cuda")
+    _, _, qc, _, qh, _ = bs.fp8_gated_backward(dh, gu, bs.ACT_GELU)
+    zero = g <= -5.17
+    for q in (qh[:, 0], qc[:N, 0], qc[N:, 0]):
+        assert bool(((ref.decode(q) == 0) == zero).all())
 
 
 @pytest.mark.parametrize("sizes", [[5], [0, 0], [0, 1, 127, 128, 0, 129], [300, 2], [3] * 70 + [200] + [1] * 600])
