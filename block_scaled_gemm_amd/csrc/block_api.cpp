@@ -185,6 +185,10 @@ int gated_backward(int64_t M, int64_t N, int G, const int32_t* offsets, int64_t 
     if (M > 0 && N > 0 && (!dh || !gu || (!qr && !qc && !qh))) return FP8BS_ERR_ARG;
     if ((qr && !sr) || (qc && !sc) || (qh && !sh)) return FP8BS_ERR_ARG;
     if (N % 128 != 0) return FP8BS_ERR_SHAPE;
+    // 32-bit offsets inside a tile of 128 rows or columns
+    if (lddh > FP8BS_MAX_LD || ldgu > FP8BS_MAX_LD || (qr && ldqr > FP8BS_MAX_LD) || (qc && ldqc > FP8BS_MAX_LD) ||
+        (qh && ldqh > FP8BS_MAX_LD))
+        return FP8BS_ERR_SHAPE;
     if (lddh < N || ldgu < 2 * N || (qr && (ldqr < 2 * N || ldsr < M)) ||
         (qc && (ldqc < bound || ldsc < 2 * N)) || (qh && (ldqh < bound || ldsh < N)))
         return FP8BS_ERR_ARG;

@@ -1020,14 +1020,24 @@ hipError_t launch_grouped_gated(const GatedArgs& g, hipStream_t st) {
 
 constexpr int BT = THREADS;
 
-// Max over the four 16-lane DPP rows of the wave, lane by lane, of values >= 0
-// (gfx950's row and half-wave swaps: both results hold one of the two sides).
-__device__ __forceinline__ float rows4_max(float f) {
-    uint32_t v = __float_as_uint(f);
-    auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = max((uint32_t)a[0], (uint32_t)a[1]);
-    auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return __uint_as_float(max((uint32_t)b[0], (uint32_t)b[1]));
+// Column maxima (values >= 0) over the wave's four 16-lane DPP rows, eight
+// columns at once: a swap of half-waves (then of rows) between the registers
+// of two columns leaves each lane with one column's two sides, so every step
+// halves the registers.  Lane in row q ends with columns 2q and 2q + 1.
+__device__ __forceinline__ float2 rows4_max(const float (&m)[8]) {
+    float h[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {  // low half: column k, high half: k + 4
+        auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(m[k]), __float_as_uint(m[k + 4]), false, false);
+        h[k] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    }
+    float r[2];
+#pragma unroll
+    for (int k = 0; k < 2; k++) {  // rows 0..3: columns k, k + 2, k + 4, k + 6
+        auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(h[k]), __float_as_uint(h[k + 2]), false, false);
+        r[k] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    }
+    return make_float2(r[0], r[1]);
 }
 
 __device__ __forceinline__ float amax2(float a, float b) { return fmaxf(fabsf(a), fabsf(b)); }
@@ -1077,12 +1087,12 @@ __global__ __launch_bounds__(BT) __attribute__((amdgpu_waves_per_eu(4, 4))) void
     uint4 vd[4], vg[4], vu[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const int r = 4 * rg + i < rows ? 4 * rg + i : rows - 1;
-        const uint16_t* d = p.dh + (row0 + r) * p.lddh + c0 + 8 * cc;
-        const uint16_t* g = p.gu + (row0 + r) * p.ldgu + c0 + 8 * cc;
-        vd[i] = ld_stream(d);
-        vg[i] = ld_stream(g);
-        vu[i] = ld_stream(g + p.N);
+        // (32-bit offsets from wave-uniform bases: leading dimensions are at most 2^24)
+        const uint32_t r = 4 * rg + i < rows ? 4 * rg + i : rows - 1;
+        const uint32_t g = r * (uint32_t)p.ldgu + 8 * cc;
+        vd[i] = ld_stream(p.dh + row0 * p.lddh + c0 + r * (uint32_t)p.lddh + 8 * cc);
+        vg[i] = ld_stream(p.gu + row0 * p.ldgu + c0 + g);
+        vu[i] = ld_stream(p.gu + row0 * p.ldgu + p.N + c0 + g);
     }
     if (rows < 128) {  // rows past the end: zeros, so zero codes
 #pragma unroll
@@ -1124,7 +1134,7 @@ __global__ __launch_bounds__(BT) __attribute__((amdgpu_waves_per_eu(4, 4))) void
                                        fmaxf(amax2(v[4], v[5]), amax2(v[6], v[7])));
                 const GroupScale gs = group_scale(row16_max(__float_as_uint(am)), POW2);
                 if (r < rows) {
-                    st_stream8(p.qr + (row0 + r) * p.ldqr + w * p.N + c0 + 8 * cc,
+                    st_stream8(p.qr + row0 * p.ldqr + w * p.N + c0 + (uint32_t)r * (uint32_t)p.ldqr + 8 * cc,
                                pack4_scaled(v[0] * gs.inv, v[1] * gs.inv, v[2] * gs.inv, v[3] * gs.inv),
                                pack4_scaled(v[4] * gs.inv, v[5] * gs.inv, v[6] * gs.inv, v[7] * gs.inv));
                     if (cc == 0) p.sr[((w * p.N + c0) >> 7) * p.ldsr + row0 + r] = gs.s;
@@ -1141,11 +1151,8 @@ __global__ __launch_bounds__(BT) __attribute__((amdgpu_waves_per_eu(4, 4))) void
         float cm[8];
 #pragma unroll
         for (int k = 0; k < 8; k++)
-            cm[k] = rows4_max(w == 2 ? hm[k] : fmaxf(amax2(x[w][0][k], x[w][1][k]), amax2(x[w][2][k], x[w][3][k])));
-        if (lane < 16) {
-            *(float4*)&wmax[w][wave][8 * cc] = make_float4(cm[0], cm[1], cm[2], cm[3]);
-            *(float4*)&wmax[w][wave][8 * cc + 4] = make_float4(cm[4], cm[5], cm[6], cm[7]);
-        }
+            cm[k] = w == 2 ? hm[k] : fmaxf(amax2(x[w][0][k], x[w][1][k]), amax2(x[w][2][k], x[w][3][k]));
+        *(float2*)&wmax[w][wave][8 * cc + 2 * (lane >> 4)] = rows4_max(cm);
     }
     __syncthreads();
     if (t < 384) {
@@ -1188,7 +1195,7 @@ __global__ __launch_bounds__(BT) __attribute__((amdgpu_waves_per_eu(4, 4))) void
 #pragma unroll
         for (int k = 0; k < 2; k++) {
             const int id = k * BT + t, col = id >> 3, ch = id & 7;
-            *(uint4*)(q + col * ldq + pg * 128 + 16 * ch) =
+            *(uint4*)(q + pg * 128 + (uint32_t)col * (uint32_t)ldq + 16 * ch) =
                 *(const uint4*)&codes[col * 32 + ((ch ^ ((col >> 3) & 7)) << 2)];
         }
         __syncthreads();

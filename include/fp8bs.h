@@ -590,7 +590,8 @@ int fp8_grouped_gated_gemm_quant(int G, int64_t rows_bound, int64_t N,
  * The quantised values have to be finite, as for every quantiser here.
  * N a multiple of 128.  Alignment: dh, gu, qr, qc, qh 16-byte aligned; lddh,
  * ldgu multiples of 8; ldqr, ldqc, ldqh of 16; scales 4-byte aligned.
- * lddh >= N; ldgu, ldqr, ldsc >= 2N; ldsr >= M; ldsh >= N.
+ * lddh >= N; ldgu, ldqr, ldsc >= 2N; ldsr >= M; ldsh >= N; lddh, ldgu, ldqr,
+ * ldqc, ldqh <= FP8BS_MAX_LD.
  * Errors: ERR_ARG, ERR_SHAPE, ERR_ALIGN, ERR_DEVICE, ERR_HIP.
  */
 int fp8_gated_backward(int64_t M, int64_t N, const uint16_t *dh, int64_t lddh,

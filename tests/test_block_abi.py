@@ -92,6 +92,8 @@ BWD_COMMON = [
     (dict(ldsh=128), ARG), (dict(dh=FAKE + 8), ALIGN), (dict(gu=FAKE + 8), ALIGN), (dict(qr=FAKE + 8), ALIGN),
     (dict(qc=FAKE + 8), ALIGN), (dict(qh=FAKE + 4), ALIGN), (dict(sc=FAKE + 2), ALIGN), (dict(lddh=260), ALIGN),
     (dict(ldgu=516), ALIGN), (dict(ldqr=520), ALIGN), (dict(N=0), OK),
+    (dict(lddh=(1 << 24) + 8), SHAPE), (dict(ldgu=(1 << 24) + 8), SHAPE), (dict(ldqr=(1 << 24) + 16), SHAPE),
+    (dict(ldqc=(1 << 24) + 16), SHAPE), (dict(ldqh=(1 << 24) + 16), SHAPE),
 ]
 
 
