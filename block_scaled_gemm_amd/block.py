@@ -369,6 +369,8 @@ def fp8_norm_residual(x, w_pre=None, y=None, w_post=None, gate=None, gate_rows=N
     if w_post is None:
         ry = None
     if w_pre is None:
+        if want_h or h is not None or q is not None or s is not None:
+            raise ValueError("h and its codes need w_pre")
         rx = None
     else:
         prep = _arg(w_pre, "w_pre", F32, dev, (D,))[0]

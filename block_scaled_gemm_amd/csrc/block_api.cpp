@@ -15,9 +15,8 @@ using namespace fp8bs_api;
 
 namespace {
 
-// Bytes between the gate's and the up's block scalars, and element offsets
-// inside a tile, are 32-bit in the kernels.
-constexpr int64_t kMaxScaleSpan = 1LL << 30;
+// The bytes between the gate's and the up's block scalars are a 32-bit offset.
+constexpr int64_t kMaxScaleSpan = (1LL << 30) - 1;
 constexpr int64_t kMaxGrid = (1LL << 31) - 1;  // workgroups of one launch
 
 bool bad_act(int act) { return act != FP8BS_ACT_SILU && act != FP8BS_ACT_GELU; }

@@ -515,7 +515,7 @@ int fp8_grouped_gemm_strided(int G, int64_t rows_bound, int64_t N, int64_t K,
  * Alignment: a, b, d, gu 16-byte aligned; lda, ldb multiples of 16 (K > 0);
  * ldd a multiple of 4, ldgu of 8; sa, sb 4-byte aligned.  lda, ldb >= K and
  * <= FP8BS_MAX_LD; ldsa >= M; ldsb >= K/128; ldd >= N; ldgu >= 2N.
- * Errors: ERR_ARG, ERR_SHAPE (also (N/128) * ldsb above 2^30), ERR_ALIGN,
+ * Errors: ERR_ARG, ERR_SHAPE (also (N/128) * ldsb >= 2^30), ERR_ALIGN,
  * ERR_WORKSPACE, ERR_DEVICE, ERR_HIP.
  */
 int fp8_gated_gemm(int64_t M, int64_t N, int64_t K, const uint8_t *a,

@@ -26,7 +26,8 @@ COMMON = [
     (dict(act=2), ARG), (dict(acc=3), ARG), (dict(M=-1), ARG), (dict(a=None), ARG), (dict(sa=None), ARG),
     (dict(b=None), ARG), (dict(sb=None), ARG), (dict(lda=256), ARG), (dict(ldb=256), ARG), (dict(ldsa=63), ARG),
     (dict(ldsb=3), ARG), (dict(gu=FAKE, ldgu=504), ARG), (dict(K=500), SHAPE), (dict(N=200), SHAPE),
-    (dict(lda=(1 << 24) + 16), SHAPE), (dict(ldb=(1 << 24) + 16), SHAPE), (dict(ldsb=1 << 30), SHAPE),
+    (dict(lda=(1 << 24) + 16), SHAPE), (dict(ldb=(1 << 24) + 16), SHAPE), (dict(ldsb=1 << 30), SHAPE), (dict(ldsb=1 << 29), SHAPE),
+    (dict(ldsb=(1 << 29) - 1, M=0), OK),
     (dict(a=FAKE + 8), ALIGN), (dict(b=FAKE + 8), ALIGN), (dict(sa=FAKE + 2), ALIGN), (dict(sb=FAKE + 2), ALIGN),
     (dict(gu=FAKE + 8, ldgu=512), ALIGN), (dict(gu=FAKE, ldgu=516), ALIGN), (dict(lda=520), ALIGN),
     (dict(ldb=520), ALIGN), (dict(M=0), OK), (dict(N=0), OK),

@@ -193,7 +193,7 @@ def test_binding_refusals(hip):
     b = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
     v = torch.ones(256, device="cuda")
     for f in (lambda: bs.fp8_norm_residual(b, v[:128]), lambda: bs.fp8_norm_residual(b, v, y=b[:3]),
-              lambda: bs.fp8_norm_residual(b.float(), v),
+              lambda: bs.fp8_norm_residual(b.float(), v), lambda: bs.fp8_norm_residual(b, None, y=b, want_h=True),
               lambda: bs.fp8_norm_residual(b, v, y=b, gate=torch.ones(1, 256, device="cuda"), gate_rows=2),
               lambda: bs.fp8_norm_residual(b, v, y=b, gate=torch.ones(1, 256, device="cuda"), gate_rows=0),
               lambda: bs.fp8_norm_residual_backward(None, b, b, v, v),
