@@ -7,14 +7,16 @@
 //   r_x = 1/sqrt(mean(x'^2) + eps)  h = x' r_x w_pre
 //
 // HBM-bound: 4 B read and 2 + 1 B written per element forward, 8 B read and
-// 4 B written backward.  A workgroup holds whole rows in registers (8 columns
-// per thread and vector), so every row is read once; it walks consecutive
-// rows, so the fp32 vectors w_pre, w_post and gate are read once per
-// workgroup and stay in registers.  8192 x 7168 with everything in: forward 95
-// us (4.3 TB/s), 88 without the waits for the two row sums; backward 169 us
-// with its reduction (4.2 TB/s), 150 without them.
+// 4 B written backward.  A wave or a workgroup holds whole rows in registers (8
+// columns per thread and vector), so every row is read once; a workgroup walks
+// consecutive rows, so the fp32 vectors w_pre, w_post and gate are read once per
+// workgroup.  8192 x 7168 with everything in: forward 86 us (4.8 TB/s, 81
+// without storing the scales); backward 169 us with its reduction (4.2 TB/s),
+// 150 without the waits for its row sums.
 #include "block_kernels.h"
 #include "device.h"
+
+#include <type_traits>
 
 namespace fp8bs {
 
@@ -68,8 +70,9 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*lds)[16][N], in
 }
 
 // Rows stream through once, so their loads and stores are non-temporal (norm
-// of 8192 x 7168: 101 -> 95 us, its backward 172 -> 169).  raw8: eight bf16 as loaded; widening them is
-// put off so that the next row's wait in half the registers.
+// of 8192 x 7168, a row to a workgroup: 101 -> 95 us, its backward 172 -> 169).
+// raw8: eight bf16 as loaded; widening them is put off so that the next row's
+// wait in half the registers.
 typedef uint32_t u32x4_n __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_n __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint4 raw8(const uint16_t* p, bool on) {
@@ -90,8 +93,8 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
 
 constexpr int NORM_ROWS = 16;  // most rows of a workgroup
 
-// Thread t owns columns 8(t + j*threads) ..+7, j < NV.  The next row is loaded
-// before this one's sums.  gw holds gate * w_post (or the one there is).
+// A row to each workgroup.  Thread t owns columns 8(t + j*threads) ..+7, j < NV.
+// The next row is loaded before this one's sums.  gw holds gate * w_post (or the one there is).
 template <int NV, int MAXT>
 __global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs p, int64_t rows_per) {
     __shared__ float red[2][16][1];
@@ -203,16 +206,215 @@ __global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs p, int64_t rows_per
         if (i % NORM_ROWS < rows) p.s[i / NORM_ROWS * p.lds + r0 + i % NORM_ROWS] = scales[i % NORM_ROWS][i / NORM_ROWS];
 }
 
+// A row to each wave, for launches of many rows: lane t owns columns
+// 8(t + 64j) ..+7, j < NV, so both row sums stay in the wave and no wave waits
+// for another; the next row's vectors are loaded as the quantisation of this
+// row frees their registers.  w_pre and gate * w_post are in LDS, the two
+// halves of a lane's eight columns apart so that a wave's 16-byte reads are
+// contiguous.  A row of another gate row than the workgroup's first takes gate
+// and w_post from memory.  The rows of a workgroup are consecutive so that a
+// group's scales leave in whole lines (rows dealt out over the chip, scales
+// stored one by one: 8192 x 7168 104 us).
+constexpr int NORM_WAVE_ROWS = 32;  // most rows of a workgroup
+
+__device__ __forceinline__ void lds_f8(const float4 (&v)[2][64], int lane, float (&f)[8]) {
+    const float4 a = v[0][lane], b = v[1][lane];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+template <int NV, bool Y, bool PRE, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void norm_wave_kernel(NormArgs p, int64_t rows_per) {
+    __shared__ float4 wpre[PRE ? NV : 1][2][64], gw[Y ? NV : 1][2][64];
+    __shared__ float scales[NORM_WAVE_ROWS][4 * NV + 1];
+    const int t = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // rows in scalar registers
+    const int64_t r0 = blockIdx.x * rows_per, r1 = r0 + rows_per < p.M ? r0 + rows_per : p.M;
+    const float inv_d = 1.0f / (float)p.D;
+    const int D = (int)p.D;
+    // the factor of y r_y at eight columns
+    auto factor = [&](const float* gate, int col, float (&f)[8]) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) f[k] = 1.0f;
+        if (gate) loadf8(gate + col, true, f);
+        if (p.w_post) {
+            float w[8];
+            loadf8(p.w_post + col, true, w);
+#pragma unroll
+            for (int k = 0; k < 8; k++) f[k] *= w[k];
+        }
+    };
+    const int64_t gate0 = Y && p.gate ? r0 / p.gate_rows : 0;
+    const int64_t gate_end = Y && p.gate ? (gate0 + 1) * p.gate_rows : p.M;  // rows before it take gw from LDS
+    // the last two vectors may lie past D: such lanes load column 0 and count for nothing
+    auto on = [&](int j) { return j < NV - 2 || 8 * (t + 64 * j) < D; };
+    uint4 rx[NV], ry[Y ? NV : 1];
+    auto load = [&](int j, int64_t r) {
+        const int at = on(j) ? 8 * t + 512 * j : 0;
+        rx[j] = raw8(p.x + r * p.ldx + at, true);
+        if constexpr (Y) ry[j] = raw8(p.y + r * p.ldy + at, true);
+    };
+    if (r0 + wave < r1)
+#pragma unroll
+        for (int j = 0; j < NV; j++) load(j, r0 + wave);
+    for (int v = threadIdx.x; v < D / 8; v += 64 * WAVES) {
+        float f[8];
+        if constexpr (PRE) {
+            loadf8(p.w_pre + 8 * v, true, f);
+            wpre[v >> 6][0][v & 63] = make_float4(f[0], f[1], f[2], f[3]);
+            wpre[v >> 6][1][v & 63] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+        if constexpr (Y) {
+            factor(p.gate ? p.gate + gate0 * p.D : nullptr, 8 * v, f);
+            gw[v >> 6][0][v & 63] = make_float4(f[0], f[1], f[2], f[3]);
+            gw[v >> 6][1][v & 63] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+    }
+    __syncthreads();
+    for (int64_t r = r0 + wave; r < r1; r += WAVES) {
+        float x[NV][8], sx = 0.f;
+        int lane = t;  // anew in each row: the vectors in LDS are not to move to registers
+        asm volatile("" : "+v"(lane));
+        auto add_squares = [&](int j) {  // a vector's eight, then over the vectors
+            float v = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; k++) v += x[j][k] * x[j][k];
+            sx += on(j) ? v : 0.f;
+        };
+        if constexpr (Y) {
+            float ys = 1.0f;
+            if (p.w_post) {
+                float sy = 0.f;
+#pragma unroll
+                for (int j = 0; j < NV; j++) {
+                    float y[8], v = 0.f;
+                    widen8(ry[j], y);
+#pragma unroll
+                    for (int k = 0; k < 8; k++) v += y[k] * y[k];
+                    sy += on(j) ? v : 0.f;
+                    // y stays packed until it is used again
+                    asm volatile("" : "+v"(ry[j].x), "+v"(ry[j].y), "+v"(ry[j].z), "+v"(ry[j].w));
+                }
+                ys = 1.0f / sqrtf(wave_sum(sy) * inv_d + p.eps);
+                if (t == 0 && p.rstd_y) p.rstd_y[r] = ys;
+            }
+            auto residual = [&](auto in_lds) {
+                const float* gate = in_lds ? nullptr : p.gate + r / p.gate_rows * p.D;
+#pragma unroll
+                for (int j = 0; j < NV; j++) {
+                    float y[8], f[8];
+                    if (in_lds)
+                        lds_f8(gw[j], lane, f);
+                    else
+                        factor(gate, on(j) ? 8 * lane + 512 * j : 0, f);
+                    widen8(rx[j], x[j]);
+                    widen8(ry[j], y);
+#pragma unroll
+                    for (int k = 0; k < 8; k++) x[j][k] = p.alpha * x[j][k] + y[k] * ys * f[k];
+                    if (on(j)) store8(p.xo + r * p.ldxo + 8 * t + 512 * j, x[j]);
+                    add_squares(j);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            if (r < gate_end)
+                residual(std::true_type{});
+            else
+                residual(std::false_type{});
+        } else {
+#pragma unroll
+            for (int j = 0; j < NV; j++) {
+                widen8(rx[j], x[j]);
+                add_squares(j);
+            }
+        }
+        if constexpr (!PRE) {
+            if (r + WAVES < r1)
+#pragma unroll
+                for (int j = 0; j < NV; j++) load(j, r + WAVES);
+        } else {
+            // the norm takes x' in fp32, before its rounding for the residual stream
+            const float xs = 1.0f / sqrtf(wave_sum(sx) * inv_d + p.eps);
+            if (t == 0 && p.rstd_x) p.rstd_x[r] = xs;
+            auto norm = [&](auto more) {
+#pragma unroll
+                for (int j = 0; j < NV; j++) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    float h[8], am = 0.f;
+                    lds_f8(wpre[j], lane, h);
+#pragma unroll
+                    for (int k = 0; k < 8; k++) {
+                        h[k] = x[j][k] * xs * h[k];
+                        am = fmaxf(am, fabsf(h[k]));
+                    }
+                    if (more) load(j, r + WAVES);
+                    if (p.q) {
+                        // 16 lanes hold a group; lanes past D are whole groups
+                        const GroupScale gs = group_scale(row16_max(__float_as_uint(am)), p.pow2);
+                        if (on(j)) {
+                            const u32x2_n c = {pack4(h[0] * gs.inv, h[1] * gs.inv, h[2] * gs.inv, h[3] * gs.inv),
+                                               pack4(h[4] * gs.inv, h[5] * gs.inv, h[6] * gs.inv, h[7] * gs.inv)};
+                            __builtin_nontemporal_store(c, (u32x2_n*)(p.q + r * p.ldq + 8 * t + 512 * j));
+                            if ((t & 15) == 0) scales[r - r0][4 * j + (t >> 4)] = gs.s;
+                        }
+                    }
+                    if (p.h && on(j)) store8(p.h + r * p.ldh + 8 * t + 512 * j, h);
+                }
+            };
+            if (r + WAVES < r1)
+                norm(std::true_type{});
+            else
+                norm(std::false_type{});
+        }
+    }
+    if (!p.q) return;
+    __syncthreads();
+    const int rows = (int)(r1 - r0), groups = D >> 7;
+    for (int i = threadIdx.x; i < NORM_WAVE_ROWS * groups; i += 64 * WAVES)
+        if (i % NORM_WAVE_ROWS < rows)
+            p.s[i / NORM_WAVE_ROWS * p.lds + r0 + i % NORM_WAVE_ROWS] = scales[i % NORM_WAVE_ROWS][i / NORM_WAVE_ROWS];
+}
+
+// A workgroup's waves: eight, but four where the row's vectors with y need more
+// than 256 registers (4096 x 8192: 51 us, eight with spills 61).  Workgroups:
+// as many as the registers let run at once.
+template <int NV, bool Y, bool PRE>
+static void launch_norm_rows(const NormArgs& g, hipStream_t st) {
+    constexpr int WAVES = Y && NV > 14 ? 4 : 8;
+    const int64_t at_once = NV <= 4 ? 512 : 256;
+    int64_t rows_per = (g.M + at_once - 1) / at_once;
+    if (rows_per > NORM_WAVE_ROWS) rows_per = NORM_WAVE_ROWS;
+    const dim3 grid((unsigned)((g.M + rows_per - 1) / rows_per));
+    hipLaunchKernelGGL((norm_wave_kernel<NV, Y, PRE, WAVES>), grid, dim3(64 * WAVES), 0, st, g, rows_per);
+}
+
+template <int NV = 16>
+static void launch_norm_wave(const NormArgs& g, hipStream_t st) {
+    if constexpr (NV > 2) {
+        if (g.D <= 512 * (NV - 2)) return launch_norm_wave<NV - 2>(g, st);
+    }
+    if (!g.y)
+        launch_norm_rows<NV, false, true>(g, st);
+    else if (g.w_pre)
+        launch_norm_rows<NV, true, true>(g, st);
+    else
+        launch_norm_rows<NV, true, false>(g, st);
+}
+
 // Threads (a multiple of 64) that hold D columns in nv vectors of 8.
 static int norm_threads(int64_t D, int nv) { return (int)((D / 8 + nv - 1) / nv + 63) / 64 * 64; }
 
-// Two vectors a thread from 4096 columns on: 14 waves a row leave room for one
-// workgroup per CU, whose row sums nothing overlaps (8192 x 7168: 100 us
-// against 95 with 7 waves; 4096 x 8192 52 against 54).  Rows per workgroup, a
-// power of two: as many as leave 14 waves on every CU (8192 x 7168 in 4, 8, 16
-// rows: 111, 98, 95 us; 8192 x 2048: 29, 27, 32 us).
+// A row to a wave where there are 1024 rows or more (4096, 2048, 1024 rows of
+// 7168: 44, 22, 15 us against 52, 29, 15 of a row to a workgroup; 8192 x 2048 25
+// against 27; 32768 x 4096 175 against 189; norm alone of 8192 x 7168 37 against
+// 42).  Fewer rows and rows wider than 8192 take a workgroup's registers for a
+// row, two vectors a thread from 4096 columns on (14 waves would leave room for
+// one workgroup per CU, whose row sums nothing overlaps), and walk as many rows,
+// a power of two, as leave 14 waves on every CU.
 hipError_t launch_norm(const NormArgs& g, hipStream_t st) {
     if (g.M == 0 || g.D == 0) return hipSuccess;
+    if (g.M >= 1024 && g.D <= 8192) {
+        launch_norm_wave(g, st);
+        return hipGetLastError();
+    }
     const int nv = g.D <= 4096 ? 1 : g.D <= 8192 ? 2 : 4;
     const dim3 nt(norm_threads(g.D, nv));
     int64_t rows_per = 1;

@@ -91,6 +91,63 @@ def test_pre_norm_alone(hip, M, D):
     assert r.xo is None and r.rstd_y is None and (r.q is None) == (D % 128 != 0)
 
 
+# launches of many rows: column counts on both sides of a wave's vector counts,
+# the last rows of a workgroup, gate rows of one row, within and across workgroups
+MANY = [(1024, 136, 5), (1031, 512, 1), (1025, 520, 1025), (2051, 1024, 7), (1500, 1920, 300), (1029, 2176, 64),
+        (1024, 4096, 4), (1033, 5248, 33), (1027, 7168, 257), (1030, 8192, 2)]
+
+
+@pytest.mark.parametrize("M,D,rows", MANY)
+def test_forward_many_rows(hip, M, D, rows):
+    codes = D % 128 == 0
+    for post, gated, alpha in ((True, True, -0.5), (True, False, 1.0), (False, True, 1.0), (False, False, 2.0)):
+        c = make(M, D, post, gated, rows, M + D + 7)
+        gate = ref.gate_rows_of(up(c["gate"]), rows, M) if gated else None
+        xo, h, ry, rx = ref.norm(up(c["x"]), up(c["y"]), up(c["w_post"]), gate, alpha, up(c["w_pre"]))
+        ex, eh, rel = forward_bounds(c, xo, h, rx, gate, alpha, up(c["y"]), ry)
+        kw = dict(y=dev(c["y"]), w_post=dev(c["w_post"]), gate=dev(c["gate"]), gate_rows=rows if gated else None,
+                  alpha=alpha)
+        r = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), want_h=True, quantise=codes, **kw)
+        near(r.xo, xo, ex, UBF16, "x'")
+        near(r.h, h, eh, UBF16, "h")
+        near(r.rstd_x, rx, rel * rx, U32, "r_x")
+        if post:
+            near(r.rstd_y, ry, SUM * ry, U32, "r_y")
+        if codes:
+            ref.check_groups(r.q, r.s.t(), h, eh, False, "codes")
+        # x' is the same without the next norm, and in place
+        x = dev(c["x"]).clone()
+        bs.fp8_norm_residual(x, None, xo=x, **kw)
+        assert torch.equal(x, r.xo)
+        # the backward pass takes the forward's statistics
+        b = bs.fp8_norm_residual_backward(dev(c["dxo"]), dev(c["dh"]), r.xo, r.rstd_x, dev(c["w_pre"]),
+                                          rstd_y=r.rstd_y, **kw)
+        backward_checks(c, M, D, rows, post, gated, alpha, True, True, b, up(r.xo.cpu()), up(r.rstd_x.cpu()),
+                        up(r.rstd_y.cpu()) if post else None)
+
+
+def test_many_rows_alone_and_strided(hip):
+    M, D = 1100, 1152
+    c = make(M, D, True, False, 1, 77)
+    _, h, _, rx = ref.norm(up(c["x"]), w_pre=up(c["w_pre"]))
+    r = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), want_h=True)
+    near(r.h, h, 2 * SUM * h.abs(), UBF16, "h")
+    near(r.rstd_x, rx, SUM * rx, U32, "r_x")
+    ref.check_groups(r.q, r.s.t(), h, 2 * SUM * h.abs(), False, "codes")
+    wide = lambda t, fill: torch.cat([t, torch.full((M, 8), fill, dtype=t.dtype)], 1).cuda()[:, :D]  # noqa: E731
+    nan = float("nan")
+    kw = dict(w_post=dev(c["w_post"]))
+    want = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), y=dev(c["y"]), want_h=True, **kw)
+    xo, h = torch.full((M, D + 8), 5.0).bfloat16().cuda(), torch.full((M, D + 16), 5.0).bfloat16().cuda()
+    q = torch.full((M, D + 16), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.full((D // 128, M + 3), 5.0, device="cuda")
+    bs.fp8_norm_residual(wide(c["x"], nan), dev(c["w_pre"]), y=wide(c["y"], nan), xo=xo[:, :D], h=h[:, :D], q=q[:, :D],
+                         s=s, **kw)
+    assert torch.equal(xo[:, :D], want.xo) and torch.equal(h[:, :D], want.h) and torch.equal(q[:, :D], want.q)
+    assert torch.equal(s[:, :M], want.s) and bool((s[:, M:] == 5).all()) and bool((q[:, D:] == 0x55).all())
+    assert bool((xo[:, D:] == 5).all()) and bool((h[:, D:] == 5).all())
+
+
 def test_zero_and_infinite_rows(hip):
     """A zero row gives zeros; an infinity or NaN stays in its row."""
     M, D = 6, 256
