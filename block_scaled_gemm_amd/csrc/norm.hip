@@ -11,8 +11,7 @@
 // columns per thread and vector), so every row is read once; a workgroup walks
 // consecutive rows, so the fp32 vectors w_pre, w_post and gate are read once per
 // workgroup.  8192 x 7168 with everything in: forward 86 us (4.8 TB/s, 81
-// without storing the scales); backward 169 us with its reduction (4.2 TB/s),
-// 150 without the waits for its row sums.
+// without storing the scales); backward 152 us with its reduction (4.6 TB/s).
 #include "block_kernels.h"
 #include "device.h"
 
@@ -95,8 +94,8 @@ constexpr int NORM_ROWS = 16;  // most rows of a workgroup
 
 // A row to each workgroup.  Thread t owns columns 8(t + j*threads) ..+7, j < NV.
 // The next row is loaded before this one's sums.  gw holds gate * w_post (or the one there is).
-template <int NV, int MAXT>
-__global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs p, int64_t rows_per) {
+template <int NV>
+__global__ __launch_bounds__(1024) void norm_kernel(NormArgs p, int64_t rows_per) {
     __shared__ float red[2][16][1];
     // the rows' scales leave together: a group's are neighbours in memory
     __shared__ float scales[NORM_ROWS][NORM_MAX_COLS / 128 + 1];
@@ -105,20 +104,36 @@ __global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs p, int64_t rows_per
     const int64_t r0 = blockIdx.x * rows_per, r1 = r0 + rows_per < p.M ? r0 + rows_per : p.M;
     const float inv_d = 1.0f / (float)p.D;
     const bool scaled = p.gate || p.w_post;
-    int64_t col[NV];
+    constexpr bool KEEP = NV <= 2;
+    int col[NV];
     bool on[NV];
-    float wpre[NV][8], gw[NV][8];
+    float wpre[KEEP ? NV : 1][8], gw[KEEP ? NV : 1][8];
     uint4 nx[NV], ny[NV];
 #pragma unroll
     for (int j = 0; j < NV; j++) {
-        col[j] = 8 * (int64_t)(t + j * nt);
+        col[j] = 8 * (t + j * nt);
         on[j] = col[j] < p.D;
         nx[j] = raw8(p.x + r0 * p.ldx + col[j], on[j]);
         if (p.y) ny[j] = raw8(p.y + r0 * p.ldy + col[j], on[j]);
-        if (p.w_pre) loadf8(p.w_pre + col[j], on[j], wpre[j]);
-        if (p.w_post && !p.gate) loadf8(p.w_post + col[j], on[j], gw[j]);
     }
-    int64_t next_gate = p.gate ? r0 / p.gate_rows * p.gate_rows : p.M;  // first row of the next gate row
+    int64_t cur = p.gate ? r0 / p.gate_rows : 0;           // the gate row in use
+    int64_t next_gate = p.gate ? cur * p.gate_rows : p.M;  // first row of the next one
+    auto load_gw = [&](int j, float (&f)[8]) {
+        loadf8((p.gate ? p.gate + cur * p.D : p.w_post) + col[j], on[j], f);
+        if (p.gate && p.w_post) {
+            float w[8];
+            loadf8(p.w_post + col[j], on[j], w);
+#pragma unroll
+            for (int k = 0; k < 8; k++) f[k] *= w[k];
+        }
+    };
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int j = 0; j < NV; j++) {
+            if (p.w_pre) loadf8(p.w_pre + col[j], on[j], wpre[j]);
+            if (p.w_post && !p.gate) load_gw(j, gw[j]);
+        }
+    }
     for (int64_t r = r0; r < r1; r++) {
         float x[NV][8], y[NV][8];
 #pragma unroll
@@ -135,15 +150,10 @@ __global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs p, int64_t rows_per
         }
         if (p.y) {
             if (r >= next_gate) {
+                if (r > r0) cur++;
+                if constexpr (KEEP) {
 #pragma unroll
-                for (int j = 0; j < NV; j++) {
-                    loadf8(p.gate + next_gate / p.gate_rows * p.D + col[j], on[j], gw[j]);
-                    if (p.w_post) {
-                        float w[8];
-                        loadf8(p.w_post + col[j], on[j], w);
-#pragma unroll
-                        for (int k = 0; k < 8; k++) gw[j][k] *= w[k];
-                    }
+                    for (int j = 0; j < NV; j++) load_gw(j, gw[j]);
                 }
                 next_gate += p.gate_rows;
             }
@@ -160,10 +170,17 @@ __global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs p, int64_t rows_per
             }
 #pragma unroll
             for (int j = 0; j < NV; j++) {
+                float f[8];
+                if constexpr (KEEP) {
+#pragma unroll
+                    for (int k = 0; k < 8; k++) f[k] = gw[j][k];
+                } else if (scaled) {
+                    load_gw(j, f);
+                }
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
                     const float n = y[j][k] * ry;
-                    x[j][k] = p.alpha * x[j][k] + (scaled ? n * gw[j][k] : n);
+                    x[j][k] = p.alpha * x[j][k] + (scaled ? n * f[k] : n);
                 }
                 if (on[j]) store8(p.xo + r * p.ldxo + col[j], x[j]);
             }
@@ -180,10 +197,16 @@ __global__ __launch_bounds__(MAXT) void norm_kernel(NormArgs p, int64_t rows_per
         if (t == 0 && p.rstd_x) p.rstd_x[r] = rx;
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            float h[8], am = 0.f;
+            float h[8], w[8], am = 0.f;
+            if constexpr (KEEP) {
+#pragma unroll
+                for (int k = 0; k < 8; k++) w[k] = wpre[j][k];
+            } else {
+                loadf8(p.w_pre + col[j], on[j], w);
+            }
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                h[k] = x[j][k] * rx * wpre[j][k];
+                h[k] = x[j][k] * rx * w[k];
                 am = fmaxf(am, fabsf(h[k]));
             }
             if (p.q) {
@@ -407,27 +430,26 @@ static int norm_threads(int64_t D, int nv) { return (int)((D / 8 + nv - 1) / nv 
 // against 27; 32768 x 4096 175 against 189; norm alone of 8192 x 7168 37 against
 // 42).  Fewer rows and rows wider than 8192 take a workgroup's registers for a
 // row, two vectors a thread from 4096 columns on (14 waves would leave room for
-// one workgroup per CU, whose row sums nothing overlaps), and walk as many rows,
-// a power of two, as leave 14 waves on every CU.
+// one workgroup per CU, whose row sums nothing overlaps), four from 16384 on
+// (there with w_pre and gw from memory: 1024 x 32768 198 -> 105 us), and walk as
+// many rows, a power of two, as leave 14 waves on every CU.
 hipError_t launch_norm(const NormArgs& g, hipStream_t st) {
     if (g.M == 0 || g.D == 0) return hipSuccess;
     if (g.M >= 1024 && g.D <= 8192) {
         launch_norm_wave(g, st);
         return hipGetLastError();
     }
-    const int nv = g.D <= 4096 ? 1 : g.D <= 8192 ? 2 : 4;
+    const int nv = g.D <= 4096 ? 1 : g.D <= 16384 ? 2 : 4;
     const dim3 nt(norm_threads(g.D, nv));
     int64_t rows_per = 1;
     while (rows_per < NORM_ROWS && g.M * (nt.x / 64) >= rows_per * 2 * 256 * 14) rows_per *= 2;
     const dim3 grid((unsigned)((g.M + rows_per - 1) / rows_per));
     if (nv == 1)
-        hipLaunchKernelGGL((norm_kernel<1, 512>), grid, nt, 0, st, g, rows_per);
+        hipLaunchKernelGGL(norm_kernel<1>, grid, nt, 0, st, g, rows_per);
     else if (nv == 2)
-        hipLaunchKernelGGL((norm_kernel<2, 512>), grid, nt, 0, st, g, rows_per);
-    else if (nt.x <= 512)
-        hipLaunchKernelGGL((norm_kernel<4, 512>), grid, nt, 0, st, g, rows_per);
+        hipLaunchKernelGGL(norm_kernel<2>, grid, nt, 0, st, g, rows_per);
     else
-        hipLaunchKernelGGL((norm_kernel<4, 1024>), grid, nt, 0, st, g, rows_per);
+        hipLaunchKernelGGL(norm_kernel<4>, grid, nt, 0, st, g, rows_per);
     return hipGetLastError();
 }
 
@@ -462,18 +484,52 @@ __device__ __forceinline__ void storef8(float* p, const float (&v)[8]) {
     *(float4*)(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-template <int NV>
-__global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int64_t rows_per) {
+// A row to each workgroup and the next one on its way, as in norm_kernel.
+// w_pre and gw = gate * w_post (or the one there is) wait in LDS, each thread's
+// own: at 128 registers a thread there is no room for them (8192 x 7168: 168 us
+// with both in registers, 152 in LDS; two rows ahead 151; 2048 x 16384, which
+// spilled more: 358 and 147).  Two rows for one exchange of row sums spill: 197
+// us.  Rows of more than two vectors a thread would fill LDS and take them from
+// memory.
+template <int NV, int MAXT>
+__global__ __launch_bounds__(MAXT, 4) void norm_bwd_kernel(NormBwdArgs p, int64_t rows_per) {
+    __shared__ float4 own[2][NV > 2 ? 1 : NV][2][NV > 2 ? 1 : MAXT];
     __shared__ float red[2][16][3];
     int slot = 0;
     const int t = threadIdx.x, nt = blockDim.x;
     const int64_t r0 = blockIdx.x * rows_per, r1 = r0 + rows_per < p.M ? r0 + rows_per : p.M;
     const float inv_d = 1.0f / (float)p.D;
     const bool scaled = p.gate || p.w_post;
-    int64_t col[NV];
+    int col[NV];
     bool on[NV];
-    float wpre[NV][8], gw[NV][8];  // w_pre; gate * w_post, or the one there is
-    float apre[NV][8], apost[NV][8], asum[NV][8];
+    int64_t cur = p.gate ? r0 / p.gate_rows : 0;           // the gate row of `asum`
+    int64_t next_gate = p.gate ? cur * p.gate_rows : p.M;  // where the next one is taken up
+    auto load_gw = [&](int j, float (&f)[8]) {
+        loadf8((p.gate ? p.gate + cur * p.D : p.w_post) + col[j], on[j], f);
+        if (p.gate && p.w_post) {
+            float w[8];
+            loadf8(p.w_post + col[j], on[j], w);
+#pragma unroll
+            for (int k = 0; k < 8; k++) f[k] *= w[k];
+        }
+    };
+    auto put = [&](int which, int j, const float (&f)[8]) {
+        if constexpr (NV <= 2) {
+            own[which][j][0][t] = make_float4(f[0], f[1], f[2], f[3]);
+            own[which][j][1][t] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+    };
+    auto get = [&](int which, int j, float (&f)[8]) {
+        if constexpr (NV <= 2) {
+            const float4 a = own[which][j][0][t], b = own[which][j][1][t];
+            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        } else if (which == 0) {
+            loadf8(p.w_pre + col[j], on[j], f);
+        } else {
+            load_gw(j, f);
+        }
+    };
+    float apre[NV][8], asum[NV][8];
     uint4 nt_[NV], nh[NV], nx[NV], ny[NV];  // the next row's dx', dh, x', y
     auto load = [&](int64_t r) {
 #pragma unroll
@@ -488,16 +544,22 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int64_t r
     };
 #pragma unroll
     for (int j = 0; j < NV; j++) {
-        col[j] = 8 * (int64_t)(t + j * nt);
+        col[j] = 8 * (t + j * nt);
         on[j] = col[j] < p.D;
-        if (p.dh) loadf8(p.w_pre + col[j], on[j], wpre[j]);
-        if (p.w_post && !p.gate) loadf8(p.w_post + col[j], on[j], gw[j]);
+        float f[8];
+        if (p.dh) {
+            loadf8(p.w_pre + col[j], on[j], f);
+            put(0, j, f);
+        }
+        if (p.w_post && !p.gate) {
+            load_gw(j, f);
+            put(1, j, f);
+        }
 #pragma unroll
-        for (int k = 0; k < 8; k++) apre[j][k] = apost[j][k] = asum[j][k] = 0.f;
+        for (int k = 0; k < 8; k++) apre[j][k] = asum[j][k] = 0.f;
     }
     if (r0 < r1) load(r0);
-    int64_t cur = p.gate ? r0 / p.gate_rows : 0;                // the gate row of `asum`
-    int64_t next_gate = p.gate ? cur * p.gate_rows : p.M;       // where the next one is taken up
+    bool flushed = false;
     auto flush = [&](int64_t last_row) {  // gate row `cur`, whose rows here end at last_row
         const int64_t first = cur * p.gate_rows;
         const int64_t end = first + p.gate_rows < p.M ? first + p.gate_rows : p.M;
@@ -505,30 +567,33 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int64_t r
         float* to = whole ? p.dgate + cur * p.D : part_gate(p, blockIdx.x, first <= r0 ? 0 : 1);
 #pragma unroll
         for (int j = 0; j < NV; j++) {
-            float g[8], w[8];
-            loadf8(p.gate + cur * p.D + col[j], on[j], g);
-            if (p.w_post) loadf8(p.w_post + col[j], on[j], w);
+            if (on[j]) {
+                float w[8];
+                if (p.w_post) {
+                    // dw_post's partial takes the workgroup's gate rows in order
+                    float g[8], a[8];
+                    float* post = part_pre(p, blockIdx.x) + p.D + col[j];
+                    loadf8(p.gate + cur * p.D + col[j], true, g);
+                    loadf8(post, flushed, a);
+                    loadf8(p.w_post + col[j], true, w);
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                apost[j][k] += g[k] * asum[j][k];
-                w[k] = p.w_post ? w[k] * asum[j][k] : asum[j][k];
-                asum[j][k] = 0.f;
+                    for (int k = 0; k < 8; k++) {
+                        a[k] += g[k] * asum[j][k];
+                        w[k] *= asum[j][k];
+                    }
+                    storef8(post, a);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; k++) w[k] = asum[j][k];
+                }
+                storef8(to + col[j], w);
             }
-            if (on[j]) storef8(to + col[j], w);
+#pragma unroll
+            for (int k = 0; k < 8; k++) asum[j][k] = 0.f;
         }
+        flushed = true;
     };
-    for (int64_t r = r0; r < r1; r++) {
-        float dxo[NV][8], dh[NV][8], xo[NV][8], y[NV][8];
-#pragma unroll
-        for (int j = 0; j < NV; j++) {
-            widen8(nt_[j], dxo[j]);
-            if (p.dh) {
-                widen8(nh[j], dh[j]);
-                widen8(nx[j], xo[j]);
-            }
-            if (p.y) widen8(ny[j], y[j]);
-        }
-        if (r + 1 < r1) load(r + 1);
+    auto row = [&](int64_t r) {
         if (r >= next_gate) {
             if (r > r0) {
                 flush(r);
@@ -536,40 +601,52 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int64_t r
             }
 #pragma unroll
             for (int j = 0; j < NV; j++) {
-                loadf8(p.gate + cur * p.D + col[j], on[j], gw[j]);
-                if (p.w_post) {
-                    float w[8];
-                    loadf8(p.w_post + col[j], on[j], w);
-#pragma unroll
-                    for (int k = 0; k < 8; k++) gw[j][k] *= w[k];
-                }
+                float f[8];
+                load_gw(j, f);
+                put(1, j, f);
             }
             next_gate += p.gate_rows;
         }
         const float rx = p.dh ? p.rstd_x[r] : 0.f;
         const float ry = p.w_post ? p.rstd_y[r] : 1.f;
+        float g[NV][8], xh[NV][8], yh[NV][8];
         // sums of v xhat, k (dx' + r_x v), k xhat
         float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < NV; j++)
+        for (int j = 0; j < NV; j++) {
+            float w[8];
+            widen8(nt_[j], g[j]);
+            if (p.dh) {
+                float dh[8];
+                widen8(nh[j], dh);
+                widen8(nx[j], xh[j]);
+                get(0, j, w);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const float v = dh[k] * w[k];
+                    xh[j][k] *= rx;
+                    apre[j][k] += dh[k] * xh[j][k];
+                    s[0] += v * xh[j][k];
+                    g[j][k] += rx * v;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; k++) xh[j][k] = 0.f;
+            }
+            if (!p.y) continue;
+            widen8(ny[j], yh[j]);
+#pragma unroll
+            for (int k = 0; k < 8; k++) yh[j][k] *= ry;
+            if (!p.w_post) continue;
+            get(1, j, w);
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                float xhat = 0.f;
-                if (p.dh) {
-                    xhat = xo[j][k] * rx;
-                    const float v = dh[j][k] * wpre[j][k];
-                    apre[j][k] += dh[j][k] * xhat;
-                    s[0] += v * xhat;
-                    dxo[j][k] += rx * v;
-                    xo[j][k] = xhat;
-                }
-                if (p.y) y[j][k] *= ry;
-                if (p.w_post) {
-                    const float q = gw[j][k] * y[j][k];
-                    s[1] += q * dxo[j][k];
-                    s[2] += q * xhat;
-                }
+                const float q = w[k] * yh[j][k];
+                s[1] += q * g[j][k];
+                s[2] += q * xh[j][k];
             }
+        }
+        if (r + 1 < r1) load(r + 1);
         block_sum<3>(s, red, slot);
         const float c = rx * s[0] * inv_d;
         const float m = (s[1] - c * s[2]) * inv_d;
@@ -578,27 +655,35 @@ __global__ __launch_bounds__(1024) void norm_bwd_kernel(NormBwdArgs p, int64_t r
             float o[8];
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                if (p.dh) dxo[j][k] -= c * xo[j][k];
-                o[k] = p.y ? p.alpha * dxo[j][k] : dxo[j][k];
+                if (p.dh) g[j][k] -= c * xh[j][k];
+                o[k] = p.y ? p.alpha * g[j][k] : g[j][k];
             }
             if (on[j]) store8(p.dx + r * p.lddx + col[j], o);
             if (!p.y) continue;
+            if (scaled) {
+                float w[8];
+                get(1, j, w);
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                if (scaled) asum[j][k] += dxo[j][k] * y[j][k];
-                o[k] = scaled ? dxo[j][k] * gw[j][k] : dxo[j][k];
-                if (p.w_post) o[k] = ry * (o[k] - y[j][k] * m);
+                for (int k = 0; k < 8; k++) {
+                    asum[j][k] += g[j][k] * yh[j][k];
+                    o[k] = g[j][k] * w[k];
+                    if (p.w_post) o[k] = ry * (o[k] - yh[j][k] * m);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; k++) o[k] = g[j][k];
             }
             if (on[j]) store8(p.dy + r * p.lddy + col[j], o);
         }
-    }
+    };
+    for (int64_t r = r0; r < r1; r++) row(r);
     if (p.gate && r0 < r1) flush(r1);
 #pragma unroll
     for (int j = 0; j < NV; j++) {
         if (!on[j]) continue;
         float* w = part_pre(p, blockIdx.x) + col[j];
         if (p.dh) storef8(w, apre[j]);
-        if (p.w_post) storef8(w + p.D, p.gate ? apost[j] : asum[j]);
+        if (p.w_post && !p.gate) storef8(w + p.D, asum[j]);
     }
 }
 
@@ -654,19 +739,21 @@ __global__ __launch_bounds__(1024) void norm_bwd_reduce_kernel(NormBwdArgs p, in
     }
 }
 
-// One vector a thread up to 8192 columns, at 128 registers (8192 x 7168: 169
-// us; two vectors at 247 registers 208 us, with half the waves to a CU).  Rows
-// wider than that spill: a thread's two or four vectors hold 56 floats each
-// (2048 x 16384: 358 us, 1.9 TB/s).
+// One vector a thread up to 8192 columns (8192 x 7168 in two, half the waves to
+// a CU: 208 us against 169 of the kernel of then).  Wider rows spill: two vectors
+// a thread need more than its 128 registers (2048 x 16384: 147 us, 2.7 TB/s).
 static int norm_bwd_nv(int64_t D) { return D <= 8192 ? 1 : D <= 16384 ? 2 : 4; }
 
-// Workgroups: as many as run at once (16 waves a CU), so that the partials
-// stay few: each is up to 16 B per column.
+// Workgroups: as many as run at once (16 waves a CU), so that the partials,
+// each up to 16 B per column, stay few; at most two a CU (8192 x 1024 with four:
+// 37 us against 32; 32768 x 2048: 168 and 165), or four of a single wave (8192 x
+// 512: 25 us against 27).
 int norm_bwd_parts(int64_t M, int64_t D) {
     if (M == 0 || D == 0) return 0;
     const int nv = norm_bwd_nv(D);
-    int64_t per_cu = 16 / (norm_threads(D, nv) / 64 * nv);
-    if (per_cu > 4) per_cu = 4;
+    const int waves = norm_threads(D, nv) / 64;
+    int64_t per_cu = 16 / waves;
+    if (per_cu > (waves == 1 ? 4 : 2)) per_cu = waves == 1 ? 4 : 2;
     if (per_cu < 1) per_cu = 1;
     const int64_t per = (M + 256 * per_cu - 1) / (256 * per_cu);
     return (int)((M + per - 1) / per);
@@ -682,12 +769,17 @@ hipError_t launch_norm_bwd(const NormBwdArgs& g, hipStream_t st) {
     if (g.M > 0) {
         const int nv = norm_bwd_nv(g.D);
         const dim3 grid((unsigned)g.parts), nt(norm_threads(g.D, nv));
-        if (nv == 1)
-            hipLaunchKernelGGL(norm_bwd_kernel<1>, grid, nt, 0, st, g, rows_per);
+        auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, nt, 0, st, g, rows_per); };
+        if (nv == 4)
+            go(norm_bwd_kernel<4, 1024>);
         else if (nv == 2)
-            hipLaunchKernelGGL(norm_bwd_kernel<2>, grid, nt, 0, st, g, rows_per);
+            go(norm_bwd_kernel<2, 1024>);
+        else if (nt.x <= 256)
+            go(norm_bwd_kernel<1, 256>);
+        else if (nt.x <= 512)
+            go(norm_bwd_kernel<1, 512>);
         else
-            hipLaunchKernelGGL(norm_bwd_kernel<4>, grid, nt, 0, st, g, rows_per);
+            go(norm_bwd_kernel<1, 1024>);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
