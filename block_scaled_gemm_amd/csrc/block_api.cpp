@@ -103,7 +103,8 @@ int run_dense(fp8bs::GatedArgs& g, void* workspace, size_t workspace_bytes, void
 
 int run_grouped(fp8bs::GatedArgs& g, int G, const int32_t* offsets, void* stream) {
     if (G == 0 || g.M == 0 || g.N == 0) return FP8BS_OK;
-    if (fp8bs::grouped_col_bound(g.M, G) / 128 > kMaxGrid / (g.N / 128)) return FP8BS_ERR_SHAPE;
+    // (the grid is rounded up to whole turns round the XCDs)
+    if (fp8bs::grouped_col_bound(g.M, G) / 128 > (kMaxGrid - 64) / (g.N / 128)) return FP8BS_ERR_SHAPE;
     if (int r = check_device()) return r;
     g.G = G;
     g.offsets = offsets;

@@ -59,9 +59,9 @@ __device__ __forceinline__ uint32_t pk_bf16(float lo, float hi) {
 // ==== experts' row tiles =====================================================================
 //
 // Every expert's rows are cut into tiles of TILE rows from its first one on.
-// Tile `u`, counted over all experts: its expert, first row and how many rows
-// it holds (0: there is no such tile).  Called by THREADS threads; every thread
-// gets the answer.
+// Tile `u`, counted over all experts (or over their tiles of one size class):
+// its expert, first row and how many rows it holds (0: there is no such tile).
+// Called by THREADS threads; every thread gets the answer.
 
 struct RowTile {
     int64_t expert, row0;
@@ -69,24 +69,40 @@ struct RowTile {
     bool only;  // its expert's only tile
 };
 
-template <int TILE>
-__device__ __forceinline__ int64_t count_tiles(const int32_t* __restrict__ offsets, int G) {
-    __shared__ int64_t wsum[THREADS / 64];
-    const int t = threadIdx.x;
-    int64_t n = 0;
-    for (int e = t; e < G; e += THREADS) n += ((int64_t)offsets[e + 1] - offsets[e] + TILE - 1) / TILE;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) n += __shfl_xor(n, d);
-    if ((t & 63) == 0) wsum[t >> 6] = n;
-    __syncthreads();
-    n = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 64; w++) n += wsum[w];
-    return n;
+// How many tiles of size class cls an expert of n rows has: 0 those of more than
+// MID rows, 1 those of more than LOW, 2 the others.
+template <int TILE, int MID, int LOW>
+__device__ __forceinline__ int64_t class_tiles(int64_t n, int cls) {
+    const int64_t rest = n % TILE;
+    const int of = rest > MID ? 0 : rest > LOW ? 1 : 2;
+    return (cls == 0 ? n / TILE : 0) + (rest > 0 && of == cls);
 }
 
-template <int TILE>
-__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, int G, int64_t u) {
+template <int TILE, int MID, int LOW>
+__device__ __forceinline__ void count_tiles(const int32_t* __restrict__ offsets, int G, int64_t (&total)[3]) {
+    __shared__ int64_t wsum[3][THREADS / 64];
+    const int t = threadIdx.x;
+    int64_t n[3] = {0, 0, 0};
+    for (int e = t; e < G; e += THREADS)
+#pragma unroll
+        for (int c = 0; c < 3; c++) n[c] += class_tiles<TILE, MID, LOW>((int64_t)offsets[e + 1] - offsets[e], c);
+#pragma unroll
+    for (int c = 0; c < 3; c++) {
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) n[c] += __shfl_xor(n[c], d);
+        if ((t & 63) == 0) wsum[c][t >> 6] = n[c];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 3; c++) {
+        total[c] = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 64; w++) total[c] += wsum[c][w];
+    }
+}
+
+template <int TILE, int MID = 0, int LOW = 0>
+__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, int G, int64_t u, int cls = -1) {
     __shared__ int64_t wsum[THREADS / 64];
     __shared__ RowTile found;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -99,7 +115,7 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets
             lo = offsets[e];
             n = (int64_t)offsets[e + 1] - lo;
         }
-        const int64_t mine = (n + TILE - 1) / TILE;
+        const int64_t mine = cls < 0 ? (n + TILE - 1) / TILE : class_tiles<TILE, MID, LOW>(n, cls);
         int64_t incl = mine;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -116,7 +132,7 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets
         }
         incl += base;
         if (incl > u && incl - mine <= u) {
-            const int64_t at = (u - (incl - mine)) * TILE;
+            const int64_t at = cls > 0 ? n / TILE * TILE : (u - (incl - mine)) * TILE;
             found.expert = e;
             found.row0 = lo + at;
             found.rows = (int)(n - at < TILE ? n - at : TILE);
@@ -707,17 +723,31 @@ __global__ __launch_bounds__(THREADS) void gated_kernel(GatedArgs p, int64_t til
 // there can be (one more per expert than the rows fill) and the workgroups
 // past the last tile leave.  A workgroup to each row tile, and not to each
 // expert's rows, evens out experts of uneven size (32 experts, 4096 rows: 322
-// -> 243 us).
+// -> 243 us).  The tallest tiles come first, so that the last round of
+// workgroups is one of short tiles: 236 -> 218 us (8 experts, 4000 rows: 181 ->
+// 153).  Workgroups go round the XCDs; four columns of a row tile in turn are
+// one XCD's, so that its L2 serves their rows (one, two, sixteen columns: 222,
+// 220, 220 us; 8 experts, 1000 rows with sixteen 72 us against 69).
+constexpr int GROUPED_RUN = 4;
+
 template <int ACC, int TILE>
 __global__ __launch_bounds__(THREADS) void gated_grouped_kernel(GatedArgs p, int64_t tiles_n) {
     static_assert(TILE == Shape<21>::BM || (ACC != 0 && TILE == Shape<20>::BM), "the tallest row tile");
     constexpr int BYTES = TILE == 128 ? Lds<21>::BYTES : Lds<21>::BYTES > Lds<20>::BYTES ? Lds<21>::BYTES : Lds<20>::BYTES;
     static_assert(Lds<22>::BYTES <= BYTES, "every row-tile shape fits");
     __shared__ __attribute__((aligned(16))) uint8_t smem[BYTES];
-    const int64_t total = count_tiles<TILE>(p.offsets, p.G) * tiles_n;
-    if ((int64_t)blockIdx.x >= total) return;  // workgroup-uniform
-    const int64_t wid = xcd_remap(blockIdx.x, total);
-    const RowTile f = find_tile<TILE>(p.offsets, p.G, wid / tiles_n);
+    constexpr int MID = TILE == 256 ? Shape<21>::BM : ACC == 0 ? Shape<23>::BM : Shape<22>::BM;
+    constexpr int LOW = ACC == 0 ? Shape<23>::BM : Shape<22>::BM;
+    int64_t total[3];
+    count_tiles<TILE, MID, LOW>(p.offsets, p.G, total);
+    const uint32_t turn = blockIdx.x / (8 * GROUPED_RUN), slot = blockIdx.x / 8 % GROUPED_RUN;
+    const int64_t wid = ((int64_t)turn * 8 + blockIdx.x % 8) * GROUPED_RUN + slot;
+    if (wid >= (total[0] + total[1] + total[2]) * tiles_n) return;  // workgroup-uniform
+    int64_t u = wid / tiles_n;
+    int cls = 0;
+    while (cls < 2 && u >= total[cls]) u -= total[cls++];
+    const RowTile f = find_tile<TILE, MID, LOW>(p.offsets, p.G, u, cls);
+    if (f.rows <= 0) return;  // (offsets that do not ascend)
     GTile T = gated_operands(p, f.expert, (wid % tiles_n) * 128);
     T.m0 = f.row0;
     T.m_end = f.row0 + f.rows;
@@ -974,19 +1004,20 @@ static void launch_grouped_tile(const GatedArgs& g, hipStream_t st) {
     // the rows fill at most this many tiles, and a last tile for each expert
     int64_t most = (g.M + TILE - 1) / TILE + g.G;
     if (most > g.M) most = g.M;
-    const int64_t tiles_n = g.N / 128;
-    hipLaunchKernelGGL((gated_grouped_kernel<ACC, TILE>), dim3((unsigned)(tiles_n * most)), dim3(THREADS), 0, st, g,
-                       tiles_n);
+    const int64_t tiles_n = g.N / 128, turns = (tiles_n * most + 8 * GROUPED_RUN - 1) / (8 * GROUPED_RUN);
+    hipLaunchKernelGGL((gated_grouped_kernel<ACC, TILE>), dim3((unsigned)(turns * 8 * GROUPED_RUN)), dim3(THREADS), 0,
+                       st, g, tiles_n);
 }
 
 template <int ACC>
 static void launch_grouped_acc(const GatedArgs& g, hipStream_t st) {
-    // how the rows fall to the experts is not known here: half a tile over for
-    // each.  1 expert, 3000 rows of 2 x 2048 x 7168: 134 us on 128-row tiles, 105
-    // on 256-row ones; 8 experts, 1000 rows 72 and 95.
+    // Tall tiles unless low ones fit in one round of workgroups; how the rows fall
+    // to the experts is not known here: half a tile over for each.  (Power-of-two
+    // scales, 2 x 2048 x 7168, tall against low: 32 experts, 8192 rows 345 and 397
+    // us, 4096 rows 223 and 255, 1000 rows 143 and 141; 8 experts, 4000 rows 158
+    // and 179, and in one round, 1000 rows, 87 and 68.)
     if constexpr (ACC != 0) {
-        const int64_t tn = g.N / 128;
-        if (tall_tiles((g.M + 128 * g.G) * tn / 256, (g.M + 64 * g.G) * tn / 128, ACC)) {
+        if ((g.M + 64 * g.G) * (g.N / 128) > 128 * (int64_t)device_cus()) {
             launch_grouped_tile<ACC, 256>(g, st);
             return;
         }

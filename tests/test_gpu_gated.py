@@ -128,6 +128,17 @@ def test_grouped(hip, sizes, N, K, accum):
     assert torch.equal(h[:M], d[:M].bfloat16())
 
 
+# enough tiles for the tall ones: every size class, each side of its border, several tiles to an expert; more
+# experts than a workgroup has threads
+@pytest.mark.parametrize("accum", ["fp32", "mfma8", "pow2"])
+@pytest.mark.parametrize("sizes,N,K", [
+    ([0, 1, 64, 65, 300, 0, 128, 129, 256, 257, 320, 321, 384, 385, 0, 700], 1536, 256),
+    ([3] * 70 + [200] + [1] * 600 + [0] + [260], 128, 128),
+])
+def test_grouped_many_tiles(hip, sizes, N, K, accum):
+    test_grouped(hip, sizes, N, K, accum)
+
+
 def test_strides(hip):
     """Leading dimensions above the widths, scales of more rows than X has."""
     M, N, K = 70, 256, 384
