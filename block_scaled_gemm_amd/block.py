@@ -122,12 +122,14 @@ def _quant_out(q, s, M, N, dev, like):
 
 
 def _workspace(t, need, dev, like):
-    """(address, bytes) of device scratch, allocated where not given."""
+    """(tensor, address, bytes) of device scratch, allocated where not given.
+    The caller holds the tensor until the call is enqueued."""
     if need == 0:
-        return None, 0
+        return None, None, 0
     if t is None:
         t = torch.empty(need, dtype=U8, device=like.device)
-    return _arg(t, "workspace", U8, dev, (None,))
+        return t, t.data_ptr(), need
+    return (t, *_arg(t, "workspace", U8, dev, (None,)))
 
 
 def _stream_of(dev):
@@ -187,7 +189,7 @@ def fp8_gated_gemm(a, sa, b, sb, act=ACT_SILU, out_dtype=OUT_BF16, d=None, gu=No
     M, N, K, _, _, ops = _gated_operands(a, sa, b, sb, accum, dev)
     d, dp, ldd = _out(d, "d", F32 if out_dtype == OUT_F32 else BF16, dev, (M, N), a)
     gu, gup, ldgu = _kept(gu, save_gu, M, N, dev, a)
-    ws = _workspace(workspace, gated_workspace_bytes(M, N, K), dev, a)
+    held, *ws = _workspace(workspace, gated_workspace_bytes(M, N, K), dev, a)
     _check(lib().fp8_gated_gemm(M, N, K, *ops, act, dp, ldd, out_dtype, gup, ldgu, accum, *ws, _stream_of(dev)),
            "fp8_gated_gemm")
     return d, gu
@@ -201,7 +203,7 @@ def fp8_gated_gemm_quant(a, sa, b, sb, act=ACT_SILU, scale_mode=SCALE_FP32, q=No
     M, N, K, _, _, ops = _gated_operands(a, sa, b, sb, accum, dev)
     q, s, out = _quant_out(q, s, M, N, dev, a)
     gu, gup, ldgu = _kept(gu, save_gu, M, N, dev, a)
-    ws = _workspace(workspace, gated_workspace_bytes(M, N, K, True), dev, a)
+    held, *ws = _workspace(workspace, gated_workspace_bytes(M, N, K, True), dev, a)
     _check(lib().fp8_gated_gemm_quant(M, N, K, *ops, act, scale_mode, *out, gup, ldgu, accum, *ws, _stream_of(dev)),
            "fp8_gated_gemm_quant")
     return q, s, gu
@@ -408,7 +410,7 @@ def fp8_norm_residual_backward(dxo, dh, xo, rstd_x, w_pre, y=None, rstd_y=None, 
     dw_pre = _new((D,), F32, lead) if dh is not None else None
     dw_post = _new((D,), F32, lead) if w_post is not None else None
     dgate = torch.empty_like(gate) if gate is not None else None
-    ws = _workspace(workspace, lib().fp8_norm_backward_workspace_bytes(M, D), dev, lead)
+    held, *ws = _workspace(workspace, lib().fp8_norm_backward_workspace_bytes(M, D), dev, lead)
     _check(lib().fp8_norm_residual_backward(M, D, dxop, lddxo, dhp, lddh, xop, ldxo, rxp, prep, yp, ldy, ryp, wp, gp,
                                             rows, alpha, dxp, lddx, dyp, lddy, _ptr(dw_pre), _ptr(dw_post),
                                             _ptr(dgate), *ws, _stream_of(dev)), "fp8_norm_residual_backward")
@@ -449,7 +451,7 @@ def fp8_grad_norm(grads, workspace=None):
     dev = torch.cuda.current_device()
     (p, pp), (c, cp), (t, tp) = _host(ptr, "Q"), _host(count, "q"), _host(dtype, "i")
     norm = torch.empty(1, dtype=F32, device=dev)
-    ws = _workspace(workspace, lib().fp8_grad_workspace_bytes(len(grads)), dev, norm)
+    held, *ws = _workspace(workspace, lib().fp8_grad_workspace_bytes(len(grads)), dev, norm)
     _check(lib().fp8_grad_norm(len(grads), pp, cp, tp, norm.data_ptr(), *ws, _stream_of(dev)), "fp8_grad_norm")
     return norm
 
@@ -468,7 +470,7 @@ def fp8_grad_clip(grads, max_norm, out=None, workspace=None):
             raise ValueError("out must match grads in number, sizes and types")
     (p, pp), (c, cp), (t, tp), (o, op) = _host(ptr, "Q"), _host(count, "q"), _host(dtype, "i"), _host(optr, "Q")
     res = torch.empty(2, dtype=F32, device=dev)
-    ws = _workspace(workspace, lib().fp8_grad_workspace_bytes(len(grads)), dev, res)
+    held, *ws = _workspace(workspace, lib().fp8_grad_workspace_bytes(len(grads)), dev, res)
     at = res.data_ptr()
     _check(lib().fp8_grad_clip(len(grads), pp, cp, tp, float(max_norm), op, at, at + 4, *ws, _stream_of(dev)),
            "fp8_grad_clip")

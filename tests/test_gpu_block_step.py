@@ -228,3 +228,36 @@ def test_two_streams_at_once(hip):
     torch.cuda.synchronize()
     for h, n in got:
         assert torch.equal(h, want) and torch.equal(n.xo, wantn.xo) and torch.equal(n.q, wantn.q)
+
+
+def test_workspace_is_held_until_the_launch(hip, monkeypatch):
+    """A workspace that the binding allocates is its own until the call is
+    enqueued: what another thread allocates meanwhile lies elsewhere."""
+    import block_scaled_gemm_amd.block as block
+    real, seen = block.lib(), []
+
+    class Watched:
+        def __getattr__(self, name):
+            f = getattr(real, name)
+            if name.endswith("workspace_bytes"):
+                return f
+
+            def call(*a):
+                ptr, size = a[-3], a[-2]
+                other = torch.empty(size, dtype=torch.uint8, device="cuda")
+                seen.append((name, size > 0 and other.data_ptr() != ptr))
+                return f(*a)
+            return call
+
+    monkeypatch.setattr(block, "lib", Watched)
+    M, N, K = 40, 128, 2048
+    q, s = bs.fp8_quant_tile(torch.randn(M, K, device="cuda").bfloat16(), bs.AXIS_ROW, bs.SCALE_FP32)
+    w, sw, _ = bs.fp8_quant_block(torch.randn(2 * N, K, device="cuda").bfloat16(), bs.SCALE_FP32)
+    bs.fp8_gated_gemm(q, s, w, sw)
+    bs.fp8_gated_gemm_quant(q, s, w, sw)
+    x, one = torch.randn(300, 256, device="cuda").bfloat16(), torch.ones(256, device="cuda")
+    bs.fp8_norm_residual_backward(None, x, x, torch.ones(300, device="cuda"), one)
+    g = [torch.ones(1000, device="cuda")]
+    bs.fp8_grad_norm(g)
+    bs.fp8_grad_clip(g, 1.0)
+    assert len(seen) == 5 and all(ok for _, ok in seen), seen
