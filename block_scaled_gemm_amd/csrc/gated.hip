@@ -747,10 +747,11 @@ __global__ __launch_bounds__(THREADS) void gated_grouped_kernel(GatedArgs p, int
     int cls = 0;
     while (cls < 2 && u >= total[cls]) u -= total[cls++];
     const RowTile f = find_tile<TILE, MID, LOW>(p.offsets, p.G, u, cls);
-    if (f.rows <= 0) return;  // (offsets that do not ascend)
+    // offsets that do not ascend, or pass the rows there are
+    if (f.rows <= 0 || f.row0 >= p.M) return;
     GTile T = gated_operands(p, f.expert, (wid % tiles_n) * 128);
     T.m0 = f.row0;
-    T.m_end = f.row0 + f.rows;
+    T.m_end = f.row0 + f.rows < p.M ? f.row0 + f.rows : p.M;
     T.stream = f.only;
     const int64_t groups = p.K / 128;
     if constexpr (ACC == 0) {
@@ -1114,8 +1115,8 @@ __global__ __launch_bounds__(BT) __attribute__((amdgpu_waves_per_eu(4, 4))) void
     if (p.offsets) {
         const RowTile f = find_tile<128>(p.offsets, p.G, pg);
         row0 = f.row0;
-        rows = f.rows;
-        if (rows <= 0) return;  // workgroup-uniform: past the last group
+        rows = f.row0 + f.rows < p.M ? f.rows : (int)(p.M - f.row0);  // never past the rows there are
+        if (f.rows <= 0 || rows <= 0) return;  // workgroup-uniform: past the last group
     }
 
     uint4 vd[4], vg[4], vu[4];

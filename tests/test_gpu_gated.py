@@ -139,6 +139,31 @@ def test_grouped_many_tiles(hip, sizes, N, K, accum):
     test_grouped(hip, sizes, N, K, accum)
 
 
+def test_offsets_past_the_rows(hip):
+    """Offsets that run past rows_bound (or past T in the backward pass): the
+    rows there are come out right and nothing behind them is touched."""
+    N, K, M, bound = 256, 256, 400, 300
+    off = torch.tensor([0, 90, 390, 400], dtype=torch.int32, device="cuda")
+    qx, sx = make_x(M, K, False, 5)
+    ws = [make_w(2 * N, K, False, e) for e in range(3)]
+    qw, sw = torch.stack([w[0] for w in ws]), torch.stack([w[1] for w in ws])
+    for accum in ACCUMS.values():
+        if accum == bs.ACCUM_MFMA8_POW2:
+            continue
+        want, wgu = bs.fp8_grouped_gated_gemm(off, qx, sx, qw, sw, save_gu=True, accum=accum)
+        d = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+        gu = torch.full((M, 2 * N), 7.0, dtype=torch.bfloat16, device="cuda")
+        bs.fp8_grouped_gated_gemm(off, qx, sx, qw, sw, rows_bound=bound, d=d, gu=gu, accum=accum)
+        assert torch.equal(d[:bound], want[:bound]) and bool((d[bound:] == 7).all())
+        assert torch.equal(gu[:bound], wgu[:bound]) and bool((gu[bound:] == 7).all())
+    dh, gu = torch.randn(M, N, device="cuda").bfloat16(), wgu
+    qr, sr = torch.full((M, 2 * N), 0x55, dtype=torch.uint8, device="cuda"), torch.full((2 * N // 128, M), 7.0, device="cuda")
+    want = bs.fp8_grouped_gated_backward(off, dh, gu, with_cols=False, with_h=False)
+    bs.fp8_grouped_gated_backward(off, dh[:bound], gu[:bound], qr=qr[:bound], sr=sr, with_cols=False, with_h=False)
+    assert torch.equal(qr[:bound], want[0][:bound]) and bool((qr[bound:] == 0x55).all())
+    assert torch.equal(sr[:, :bound], want[1][:, :bound]) and bool((sr[:, bound:] == 7).all())
+
+
 def test_strides(hip):
     """Leading dimensions above the widths, scales of more rows than X has."""
     M, N, K = 70, 256, 384
