@@ -166,6 +166,29 @@ def test_zero_and_infinite_rows(hip):
         assert torch.equal(r.h[m], clean.h[m]) and torch.equal(r.xo[m], clean.xo[m])
 
 
+def test_many_rows_keep_to_themselves(hip):
+    """The same where a wave holds a row, with the infinities and NaN in the
+    columns that lanes without columns of their own read."""
+    M, D = 1100, 640
+    c = make(M, D, True, True, 50, 11)
+    x, y = c["x"].clone(), c["y"].clone()
+    x[0, 0], x[517, 1], y[518, 0], y[1099, 7] = float("inf"), float("nan"), float("nan"), float("-inf")
+    x[519] = 0
+    y[519] = 0
+    kw = dict(w_post=dev(c["w_post"]), gate=dev(c["gate"]), gate_rows=50, want_h=True)
+    r = bs.fp8_norm_residual(dev(x), dev(c["w_pre"]), y=dev(y), **kw)
+    clean = bs.fp8_norm_residual(dev(c["x"]), dev(c["w_pre"]), y=dev(c["y"]), **kw)
+    bad = torch.tensor([0, 517, 518, 1099], device="cuda")
+    assert bool((~torch.isfinite(r.h[bad])).any(1).all())
+    assert bool((r.h[519] == 0).all()) and bool((r.xo[519] == 0).all()) and bool((r.q[519] == 0).all())
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    keep[519] = False
+    for a, b in ((r.h, clean.h), (r.xo, clean.xo), (r.q, clean.q), (r.s.t(), clean.s.t()), (r.rstd_x, clean.rstd_x),
+                 (r.rstd_y, clean.rstd_y)):
+        assert torch.equal(a[keep], b[keep])
+
+
 def test_strides(hip):
     M, D = 11, 384
     c = make(M, D, True, True, 4, 5)
