@@ -20,7 +20,7 @@ constexpr int CT = 512;
 
 // 16-byte accesses, eight of a thread's in flight, non-temporal: the gradients
 // pass through once per kernel (940M fp32 elements: one in flight 2067 us,
-// eight 1940 us for both kernels, 5.8 TB/s over the three passes).
+// eight 1908 us for both kernels, 5.9 TB/s over the three passes).
 constexpr int CU = 8;
 typedef uint32_t u32x4_c __attribute__((ext_vector_type(4)));
 
